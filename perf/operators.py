@@ -182,11 +182,10 @@ def _norm_rope(x, w, s):
 def _quant(x, s):
     """fp32 [T, H, D] -> (codes as bytes, fp32 scale [T, H])."""
     f = FMAX[s["fmt"]]
-    sc = x.abs().amax(-1) / f
+    sc = (x.abs().amax(-1) / f).clamp(min=TINY)
     if s["scale"] == "ue8m0":
         m, e = torch.frexp(sc)                    # sc = m 2^e, m in [1/2, 1): an exact power of two has m = 1/2
-        sc = torch.ldexp(torch.ones_like(sc), torch.where(m == 0.5, e - 1, e).clamp(min=-126))
-    sc = sc.clamp(min=TINY)
+        sc = torch.ldexp(torch.ones_like(sc), torch.where(m == 0.5, e - 1, e))
     return (x / sc[..., None]).clamp(-f, f).to(F8[s["fmt"]]).view(torch.uint8), sc
 
 
