@@ -535,3 +535,11 @@ def moe_gemm(qa, sa, qw, sw, route: dict, stream=None):
     out = torch.empty((route["ids"].shape[0], qw.shape[1]), dtype=torch.float32, device=qa.device)
     fp8_moe_gemm(qa, sa, qw, sw, route, out, stream)
     return out
+
+
+# the paged key-value cache (its own module; the names are the package's)
+from . import kv as _kv  # noqa: E402
+from .kv import *  # noqa: E402,F401,F403
+
+__all__ += _kv.__all__
+EXPORTS += tuple(n for n in _kv.__all__ if n.startswith("fp8_")) + ("fp8_paged_attention_ws_bytes",)

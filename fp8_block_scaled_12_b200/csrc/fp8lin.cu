@@ -9,9 +9,11 @@
 #include <mutex>
 
 #include "../../include/fp8lin.h"
+#include "attn.cuh"
 #include "gemm.cuh"
 #include "gemm_mx.cuh"
 #include "gemm_swap.cuh"
+#include "kv.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -303,6 +305,148 @@ int launch_tensor_quant(const uint16_t* x, int64_t n, uint8_t* q, float* s, cuda
   if (launch(k_tensor_amax, unsigned(blocks), 256, 0, st, x, n8, slot) != cudaSuccess) return FP8_ERR_CUDA;
   if (launch(k_tensor_cast<FMT, SF>, unsigned(blocks), 256, 0, st, x, n8, slot, q) != cudaSuccess) return FP8_ERR_CUDA;
   return cuda_status(launch(k_tensor_scale<FMT, SF>, 1, 1, 0, st, slot));
+}
+
+// --------------------------------------------- paged key-value cache launches
+inline int pow2_lanes(int64_t d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+
+template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
+int launch_norm_rope_write(const KvWriteArgs& a, cudaStream_t st) {
+  constexpr int U = 2;
+  auto kern = k_norm_rope_write<LPH, U, ROPE, FMT, SF, CACHE>;
+  static std::atomic<int> occ[64];
+  const int64_t items = a.T * ((a.Hq + a.Hk + a.Hv + U - 1) / U);
+  int64_t blocks = (items + 256 / LPH - 1) / (256 / LPH);
+  const int64_t cap = int64_t(num_sms()) * resident_blocks(occ, kern, 256);
+  if (blocks > cap) blocks = cap;
+  return cuda_status(launch(kern, unsigned(blocks), 256, 0, st, a));
+}
+
+template <int ROPE, int FMT, int SF, bool CACHE>
+int launch_norm_rope_write(const KvWriteArgs& a, cudaStream_t st) {
+  switch (pow2_lanes(a.D)) {
+    case 8: return launch_norm_rope_write<8, ROPE, FMT, SF, CACHE>(a, st);
+    case 16: return launch_norm_rope_write<16, ROPE, FMT, SF, CACHE>(a, st);
+    default: return launch_norm_rope_write<32, ROPE, FMT, SF, CACHE>(a, st);
+  }
+}
+
+template <int ROPE>
+int launch_cache_write(const KvWriteArgs& a, int fmt, int scale_fmt, cudaStream_t st) {
+  if (fmt == FP8_E4M3)
+    return scale_fmt == FP8_SCALE_FP32 ? launch_norm_rope_write<ROPE, kE4M3, kScaleFp32, true>(a, st)
+                                       : launch_norm_rope_write<ROPE, kE4M3, kScaleUe8m0, true>(a, st);
+  return scale_fmt == FP8_SCALE_FP32 ? launch_norm_rope_write<ROPE, kE5M2, kScaleFp32, true>(a, st)
+                                     : launch_norm_rope_write<ROPE, kE5M2, kScaleUe8m0, true>(a, st);
+}
+
+template <int FMT>
+int launch_kv_read(const KvReadArgs& a, cudaStream_t st) {
+  static std::atomic<int> occ[64];
+  int64_t blocks = (a.rows + 7) / 8;
+  const int64_t cap = int64_t(num_sms()) * resident_blocks(occ, k_kv_read<FMT>, 256);
+  if (blocks > cap) blocks = cap;
+  return cuda_status(launch(k_kv_read<FMT>, unsigned(blocks), 256, 0, st, a));
+}
+
+// 4-D map over cache codes [pages][heads][page][dim] (any strides), box = `rows` tokens of
+// one page and head x 128 channels, 128-byte swizzle; channels from `dim` on and pages
+// outside the cache read as zeros.
+bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {cuuint64_t(c->head_dim), cuuint64_t(c->page_size), cuuint64_t(c->heads),
+                        cuuint64_t(c->num_pages)};
+  cuuint64_t strides[3] = {cuuint64_t(c->token_stride), cuuint64_t(c->head_stride), cuuint64_t(c->page_stride)};
+  cuuint32_t box[4] = {128, rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, codes, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Query heads of one kv head that a tile carries: 8, or 16 when a kv head has more.
+inline int attn_gt(int64_t G) { return G <= 8 ? 8 : 16; }
+inline int64_t attn_chunks(int64_t G) { return (G + attn_gt(G) - 1) / attn_gt(G); }
+
+// Workspace of the attention: two partial sums per CTA, then one entry per row.
+struct AttnWs {
+  int64_t o, ml, row, total;
+  AttnWs(int64_t B, int64_t H, int64_t G, int64_t D) {
+    const int64_t slots = 2 * int64_t(num_sms()), gt = attn_gt(G);
+    o = 0;
+    ml = o + slots * gt * D * 4;
+    row = ml + slots * 2 * gt * 4;
+    total = row + B * H * attn_chunks(G) * 8;
+  }
+};
+
+template <int FMT, int GT, int DCH>
+int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t st) {
+  using C = AttnCfg<GT, DCH>;
+  constexpr size_t smem = attn_smem_bytes<C>();
+  static_assert(smem <= 232448, "dynamic shared memory of one CTA (227 KB)");
+  auto kern = k_paged_attention<FMT, C>;
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0u;
+  if (bit == 0u || (ready.load(std::memory_order_acquire) & bit) == 0u) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+      return FP8_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  if (launch(kern, unsigned(grid), kAttnThreads, smem, st, mk, mv, a) != cudaSuccess) return FP8_ERR_CUDA;
+  const int heads = a.G < GT ? a.G : GT;
+  return cuda_status(launch(k_attn_join<GT>, dim3(unsigned(int64_t(a.B) * a.H * a.HC), unsigned(heads)), 128, 0, st, a));
+}
+
+template <int FMT>
+int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t st) {
+  if (attn_gt(a.G) == 8)
+    return a.D <= 128 ? launch_attention<FMT, 8, 1>(mk, mv, a, grid, st) : launch_attention<FMT, 8, 2>(mk, mv, a, grid, st);
+  return a.D <= 128 ? launch_attention<FMT, 16, 1>(mk, mv, a, grid, st) : launch_attention<FMT, 16, 2>(mk, mv, a, grid, st);
+}
+
+// Checks of a cache that every call shares.
+int check_cache(const fp8_kv_cache* c) {
+  if (!c) return FP8_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0) return FP8_ERR_INVALID_ARG;
+  if (c->fmt != FP8_E4M3 && c->fmt != FP8_E5M2) return FP8_ERR_INVALID_ARG;
+  if (c->scale_fmt != FP8_SCALE_FP32 && c->scale_fmt != FP8_SCALE_UE8M0) return FP8_ERR_INVALID_ARG;
+  if (c->head_dim % 16 != 0 || c->head_dim > 256 || c->page_size % 8 != 0) return FP8_ERR_SHAPE;
+  if (c->page_size > INT32_MAX || c->heads > 65535 || c->num_pages >= INT32_MAX) return FP8_ERR_SHAPE;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return FP8_ERR_INVALID_ARG;
+  if (c->token_stride < c->head_dim || c->head_stride < c->head_dim || c->page_stride < c->head_dim)
+    return FP8_ERR_INVALID_ARG;
+  if (c->token_stride % 16 != 0 || c->head_stride % 16 != 0 || c->page_stride % 16 != 0) return FP8_ERR_ALIGNMENT;
+  const int64_t lim = int64_t(1) << 40;
+  if (c->token_stride >= lim || c->head_stride >= lim || c->page_stride >= lim) return FP8_ERR_SHAPE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return FP8_ERR_ALIGNMENT;
+  return FP8_OK;
+}
+
+KvCache cache_of(const fp8_kv_cache* c) {
+  return KvCache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale, c->page_stride,
+                 c->head_stride, c->token_stride, c->num_pages, int(c->page_size), int(c->heads), int(c->head_dim)};
+}
+
+// A bf16 operand [T][heads][D] with token and head strides in elements.
+int check_rows(const void* p, int64_t heads, int64_t tok, int64_t head, int64_t D) {
+  if (!p) return FP8_ERR_INVALID_ARG;
+  if (tok < 0 || (heads > 1 && head < D)) return FP8_ERR_INVALID_ARG;
+  if (!aligned(p, 16) || tok % 8 != 0 || head % 8 != 0) return FP8_ERR_ALIGNMENT;
+  return FP8_OK;
+}
+
+int check_rope(int64_t R, int64_t D, const float* cos_sin, int64_t max_pos, const int64_t* pos) {
+  if (R < 0 || R > D) return FP8_ERR_INVALID_ARG;
+  if (R % 16 != 0) return FP8_ERR_SHAPE;
+  if (R > 0 && (!cos_sin || !pos || max_pos <= 0)) return FP8_ERR_INVALID_ARG;
+  if (R > 0 && (!aligned(cos_sin, 16) || !aligned(pos, 8))) return FP8_ERR_ALIGNMENT;
+  return FP8_OK;
 }
 
 // One warp whose mbarrier never completes: the bounded wait that every pipelined
@@ -649,6 +793,156 @@ int fp8_set_wait_limit_ns(int64_t limit_ns) {
   if (limit_ns < 0 || limit_ns > 10000000000ll) return FP8_ERR_INVALID_ARG;
   const unsigned long long v = limit_ns == 0 ? FP8LIN_WAIT_NS : (unsigned long long)limit_ns;
   return cuda_status(cudaMemcpyToSymbol(g_wait_limit_ns, &v, sizeof(v)));
+}
+
+int fp8_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok, int64_t k_head,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, const void* wq, const void* wk, float eps,
+                     const float* cos_sin, int64_t max_pos, int64_t R, int interleaved, const int64_t* pos, void* qo,
+                     int64_t qo_tok, int64_t qo_head, void* ko, int64_t ko_tok, int64_t ko_head, void* stream) {
+  if (T < 0 || Hq < 0 || Hk < 0 || D <= 0 || !(eps >= 0.0f) || (interleaved != 0 && interleaved != 1))
+    return FP8_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 256 || Hq > 65535 || Hk > 65535 || T > INT32_MAX) return FP8_ERR_SHAPE;
+  if (int rc = check_rope(R, D, T > 0 ? cos_sin : nullptr, T > 0 ? max_pos : 0, T > 0 ? pos : nullptr); T > 0 && rc)
+    return rc;
+  if (T == 0 || Hq + Hk == 0) return FP8_OK;
+  if (Hq > 0) {
+    if (int rc = check_rows(q, Hq, q_tok, q_head, D)) return rc;
+    if (int rc = check_rows(qo, Hq, qo_tok, qo_head, D)) return rc;
+  }
+  if (Hk > 0) {
+    if (int rc = check_rows(k, Hk, k_tok, k_head, D)) return rc;
+    if (int rc = check_rows(ko, Hk, ko_tok, ko_head, D)) return rc;
+  }
+  if ((wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return FP8_ERR_ALIGNMENT;
+  KvWriteArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_tok = q_tok, a.q_head = q_head, a.k_tok = k_tok, a.k_head = k_head;
+  a.qo = static_cast<uint16_t*>(qo);
+  a.ko = static_cast<uint16_t*>(ko);
+  a.qo_tok = qo_tok, a.qo_head = qo_head, a.ko_tok = ko_tok, a.ko_head = ko_head;
+  a.wq = static_cast<const uint16_t*>(wq);
+  a.wk = static_cast<const uint16_t*>(wk);
+  a.eps = eps;
+  a.cos_sin = cos_sin, a.max_pos = max_pos, a.pos = pos;
+  a.T = T, a.Hq = int(Hq), a.Hk = int(Hk), a.Hv = 0, a.D = int(D), a.R = int(R);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R == 0) return launch_norm_rope_write<kRopeNone, kE4M3, kScaleFp32, false>(a, st);
+  return interleaved ? launch_norm_rope_write<kRopeInterleaved, kE4M3, kScaleFp32, false>(a, st)
+                     : launch_norm_rope_write<kRopeHalves, kE4M3, kScaleFp32, false>(a, st);
+}
+
+int fp8_kv_write(const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int64_t T,
+                 const int64_t* slots, const fp8_kv_cache* cache, void* stream) {
+  return fp8_qk_norm_rope_kv_write(nullptr, 0, 0, k, k_tok, k_head, v, v_tok, v_head, T, 0, nullptr, nullptr, 0.0f,
+                                   nullptr, 0, 0, 0, nullptr, slots, cache, nullptr, 0, 0, stream);
+}
+
+int fp8_qk_norm_rope_kv_write(const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok,
+                              int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int64_t T, int64_t Hq,
+                              const void* wq, const void* wk, float eps, const float* cos_sin, int64_t max_pos,
+                              int64_t R, int interleaved, const int64_t* pos, const int64_t* slots,
+                              const fp8_kv_cache* cache, void* qo, int64_t qo_tok, int64_t qo_head, void* stream) {
+  if (T < 0 || Hq < 0 || !(eps >= 0.0f) || (interleaved != 0 && interleaved != 1)) return FP8_ERR_INVALID_ARG;
+  if (int rc = check_cache(cache)) return rc;
+  if (Hq > 65535 || T > INT32_MAX) return FP8_ERR_SHAPE;
+  if (T == 0) return FP8_OK;
+  const int64_t D = cache->head_dim;
+  if (int rc = check_rope(R, D, cos_sin, max_pos, pos)) return rc;
+  if (!slots) return FP8_ERR_INVALID_ARG;
+  if (int rc = check_rows(k, cache->heads, k_tok, k_head, D)) return rc;
+  if (int rc = check_rows(v, cache->heads, v_tok, v_head, D)) return rc;
+  if (Hq > 0) {
+    if (int rc = check_rows(q, Hq, q_tok, q_head, D)) return rc;
+    if (int rc = check_rows(qo, Hq, qo_tok, qo_head, D)) return rc;
+  }
+  if (!aligned(slots, 8) || (wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return FP8_ERR_ALIGNMENT;
+  KvWriteArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_tok = q_tok, a.q_head = q_head, a.k_tok = k_tok, a.k_head = k_head, a.v_tok = v_tok, a.v_head = v_head;
+  a.qo = static_cast<uint16_t*>(qo);
+  a.qo_tok = qo_tok, a.qo_head = qo_head;
+  a.wq = static_cast<const uint16_t*>(wq);
+  a.wk = static_cast<const uint16_t*>(wk);
+  a.eps = eps;
+  a.cos_sin = cos_sin, a.max_pos = max_pos, a.pos = pos, a.slots = slots;
+  a.c = cache_of(cache);
+  a.T = T, a.Hq = int(Hq), a.Hk = a.Hv = int(cache->heads), a.D = int(D), a.R = int(R);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R == 0) return launch_cache_write<kRopeNone>(a, cache->fmt, cache->scale_fmt, st);
+  return interleaved ? launch_cache_write<kRopeInterleaved>(a, cache->fmt, cache->scale_fmt, st)
+                     : launch_cache_write<kRopeHalves>(a, cache->fmt, cache->scale_fmt, st);
+}
+
+int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                const int32_t* offsets, int64_t B, int64_t rows, void* ko, void* vo, void* stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (B < 0 || rows < 0 || max_pages < 0 || table_stride < max_pages) return FP8_ERR_INVALID_ARG;
+  if (B > INT32_MAX || rows > INT32_MAX) return FP8_ERR_SHAPE;
+  if (B == 0 || rows == 0) return FP8_OK;
+  if ((max_pages > 0 && !table) || !offsets || !ko || !vo) return FP8_ERR_INVALID_ARG;
+  if (!aligned(table, 4) || !aligned(offsets, 4) || !aligned(ko, 16) || !aligned(vo, 16)) return FP8_ERR_ALIGNMENT;
+  KvReadArgs a{cache_of(cache), table, offsets, static_cast<uint16_t*>(ko), static_cast<uint16_t*>(vo),
+               table_stride, max_pages, rows, int(B)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->fmt == FP8_E4M3 ? launch_kv_read<kE4M3>(a, st) : launch_kv_read<kE5M2>(a, st);
+}
+
+int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache) {
+  if (B < 0 || Hq <= 0 || check_cache(cache) != FP8_OK || Hq % cache->heads != 0) return 0;
+  return AttnWs(B, cache->heads, Hq / cache->heads, cache->head_dim).total;
+}
+
+int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B, int64_t Hq, const fp8_kv_cache* cache,
+                        const int32_t* table, int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                        float scale, int64_t window, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  if (B < 0 || Hq <= 0 || max_pages < 0 || table_stride < max_pages || window < 0) return FP8_ERR_INVALID_ARG;
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return FP8_ERR_INVALID_ARG;
+  if (int rc = check_cache(cache)) return rc;
+  const int64_t H = cache->heads, D = cache->head_dim, P = cache->page_size;
+  if (Hq % H != 0) return FP8_ERR_SHAPE;
+  const int64_t G = Hq / H, HC = attn_chunks(G);
+  if (B > INT32_MAX || Hq > 65535 || B * H * HC > INT32_MAX) return FP8_ERR_SHAPE;
+  if (max_pages > INT32_MAX / P || max_pages * P > INT32_MAX - 2 * kAttnTile) return FP8_ERR_SHAPE;
+  const int64_t tiles = B * H * HC * ((max_pages * P + kAttnTile - 1) / kAttnTile + 1);
+  if (tiles > INT32_MAX) return FP8_ERR_SHAPE;
+  if (B == 0) return FP8_OK;
+  if ((max_pages > 0 && !table) || !lens || !out || !workspace) return FP8_ERR_INVALID_ARG;
+  if (int rc = check_rows(q, Hq, q_row, q_head, D)) return rc;
+  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return FP8_ERR_ALIGNMENT;
+  const AttnWs ws(B, H, G, D);
+  if (workspace_bytes < ws.total) return FP8_ERR_SHAPE;
+  int64_t br = P;                                  // rows per box: gcd(P, 128), a box never crosses a page
+  for (int64_t m = kAttnTile; m != 0;) {
+    const int64_t r = br % m;
+    br = m;
+    m = r;
+  }
+  CUtensorMap mk, mv;
+  if (!make_map_cache(&mk, cache, cache->k, uint32_t(br)) || !make_map_cache(&mv, cache, cache->v, uint32_t(br)))
+    return FP8_ERR_CUDA;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.table = table, a.lens = lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.ws_o = reinterpret_cast<float*>(w + ws.o);
+  a.ws_ml = reinterpret_cast<float*>(w + ws.ml);
+  a.ws_row = reinterpret_cast<int2*>(w + ws.row);
+  a.q_row = q_row, a.q_head = q_head, a.table_stride = table_stride;
+  a.window = window, a.cap = max_pages * P, a.pages = cache->num_pages, a.scale = scale;
+  a.B = int(B), a.H = int(H), a.G = int(G), a.HC = int(HC), a.D = int(D), a.P = int(P), a.BR = int(br);
+  const int grid = int(tiles < num_sms() ? tiles : num_sms());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->fmt == FP8_E4M3 ? launch_attention<kE4M3>(mk, mv, a, grid, st)
+                                : launch_attention<kE5M2>(mk, mv, a, grid, st);
 }
 
 int fp8_device_error(void* stream) {

@@ -156,13 +156,6 @@ struct MxArgs {
   int out_fp32;
 };
 
-// Bulk copy of `bytes` contiguous bytes global -> shared, counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 template <class C>
 __device__ __forceinline__ void mx_tile(const MxArgs& a, int t, int& p0, int& q0, int& qn) {
   if (!C::SWAP) {

@@ -332,6 +332,114 @@ int fp8_moe_gemm(const void* qa, const float* sa, const void* qw, const float* s
                  const int32_t* row_token, const float* row_weight, int64_t T, int64_t E, int64_t k, int64_t N,
                  int64_t K, float* out, void* stream);
 
+/*
+ * Paged FP8 key-value cache.  Between the two linear layers of an attention block
+ * (queries, keys and values projected by fp8_block_gemm; the output projection's input
+ * quantised by fp8_act_quant) a decoder normalises and rotates q and k, keeps k and v,
+ * and attends to what it has kept.  The cache holds codes under the rule of fp8_act_quant
+ * with one scale per token and head (the group is the head's D channels):
+ *   x ~= decode(code) * s,  s = max(fl32(amax / Fmax), 2^-126), a power of two for ue8m0.
+ * The structure is read during a call only and stays the caller's, as does the memory.
+ *   k, v        DEVICE codes: byte d of token `row` of page `page` and head `h` is at
+ *               page * page_stride + h * head_stride + row * token_stride + d, so pages
+ *               may be head-major, token-major, or hold k and v side by side.  Strides in
+ *               bytes, multiples of 16, >= head_dim, < 2^40; k, v 16-byte aligned.
+ *               Different (page, h, row) must not overlap.
+ *   k_scale, v_scale   DEVICE fp32 [num_pages][heads][page_size], 16-byte aligned.
+ *   head_dim    D % 16 == 0, D <= 256.  page_size % 8 == 0.  num_pages < 2^31 - 1.
+ *   fmt, scale_fmt   fp8_format, fp8_scale_fmt (scale_fmt matters to the writers only).
+ * No initial contents are required: readers use nothing beyond the lengths they are given.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t num_pages, page_size, heads, head_dim;
+    int64_t page_stride, head_stride, token_stride;
+    int fmt;
+    int scale_fmt;
+} fp8_kv_cache;
+
+/*
+ * fp8_qk_norm_rope -- RMS norm of every head of q and k and the position rotation, one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * w     over the head's D channels (no norm if w is NULL)
+ *   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin   for the pairs of the first R channels
+ * pairs (a, b) = (i, R/2 + i), or (2i, 2i + 1) if `interleaved`; channels >= R keep n.  All
+ * in fp32, rounded once to bf16.
+ *   q, k       bf16 [T][Hq][D], [T][Hk][D]; token and head strides in elements, multiples of
+ *              8 (views of one projection's output); 16-byte aligned.  Hq or Hk may be 0.
+ *   wq, wk     bf16 [D] or NULL; 16-byte aligned.  eps >= 0.
+ *   cos_sin    fp32 [max_pos][R]: R/2 cosines, then R/2 sines, of each position; 16-byte
+ *              aligned.  R % 16 == 0, 0 <= R <= D; R == 0: no rotation, cos_sin and pos unused.
+ *   pos        DEVICE int64 [T]; clamped into [0, max_pos).
+ *   qo, ko     bf16 outputs with strides of their own; qo may be q and ko may be k (with the
+ *              same strides), any other overlap is not allowed.
+ * Returns FP8_OK or an error status; T == 0 is a no-op.
+ */
+int fp8_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok, int64_t k_head,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, const void* wq, const void* wk, float eps,
+                     const float* cos_sin, int64_t max_pos, int64_t R, int interleaved, const int64_t* pos, void* qo,
+                     int64_t qo_tok, int64_t qo_head, void* ko, int64_t ko_tok, int64_t ko_head, void* stream);
+
+/*
+ * fp8_kv_write -- k and v of T tokens quantised into the cache.
+ *   k, v       bf16 [T][heads][D], strides as above.
+ *   slots      DEVICE int64 [T]: slot = page * page_size + row.  A slot outside
+ *              [0, num_pages * page_size) (a padding row, say -1) is skipped.  The slots of
+ *              one call must differ; which token a repeated slot holds is unspecified.
+ * Codes and scales are those of fp8_act_quant with the head as its group.
+ */
+int fp8_kv_write(const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int64_t T,
+                 const int64_t* slots, const fp8_kv_cache* cache, void* stream);
+
+/*
+ * fp8_qk_norm_rope_kv_write -- both in one pass: q as fp8_qk_norm_rope, k normalised, rotated
+ * and quantised from fp32 (rounded once), v quantised.  Arguments as above; Hq may be 0.
+ */
+int fp8_qk_norm_rope_kv_write(const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok,
+                              int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int64_t T, int64_t Hq,
+                              const void* wq, const void* wk, float eps, const float* cos_sin, int64_t max_pos,
+                              int64_t R, int interleaved, const int64_t* pos, const int64_t* slots,
+                              const fp8_kv_cache* cache, void* qo, int64_t qo_tok, int64_t qo_head, void* stream);
+
+/*
+ * fp8_kv_read -- the first tokens of B sequences back as bf16 rows, bf16_rne(decode(code) * s)
+ * (the context of a chunked prefill, say).
+ *   table      DEVICE int32 [B][max_pages], row stride table_stride >= max_pages: page ids.
+ *   offsets    DEVICE int32 [B + 1], non-decreasing: rows [offsets[b], offsets[b + 1]) of the
+ *              outputs are tokens 0, 1, ... of sequence b.
+ *   ko, vo     bf16 [rows][heads][D], 16-byte aligned.  Rows outside every range are not
+ *              written; tokens beyond the table or of a page outside the cache are zeros.
+ */
+int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_stride, int64_t max_pages,
+                const int32_t* offsets, int64_t B, int64_t rows, void* ko, void* vo, void* stream);
+
+/*
+ * fp8_paged_attention -- attention of one new token per sequence over its pages; Hq / heads
+ * query heads share a kv head (query head h reads kv head h / (Hq / heads)).
+ *   s_t = scale * q . k_t,  out = sum_t exp(s_t) v_t / sum_t exp(s_t),  lse = log sum_t exp(s_t)
+ * over the tokens t of [0, lens[b]), or the last `window` of them if window > 0.  Tokens of a
+ * page id outside [0, num_pages) are left out.  A row without any token gives zeros and
+ * lse = -infinity.  Nothing beyond these tokens matters, whatever the pages hold there.
+ *   q          bf16 [B][Hq][D], row and head strides in elements, multiples of 8; 16-byte
+ *              aligned.  Hq a multiple of cache->heads.
+ *   table      as fp8_kv_read.  lens DEVICE int32 [B], taken into [0, max_pages * page_size];
+ *              includes the new token (write it first).
+ *   out        bf16 [B][Hq][D], 16-byte aligned; lse fp32 [B][Hq] or NULL.
+ *   workspace  DEVICE scratch of at least fp8_paged_attention_ws_bytes(B, Hq, cache) bytes,
+ *              16-byte aligned, no initial contents; calls that share it must be ordered on
+ *              one stream (two captured graphs that share it must not run at once).
+ * Scores, softmax and sums are fp32; the probabilities enter the second product with 17
+ * significant bits.  The result does not depend on timing.
+ */
+int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache);
+
+int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B, int64_t Hq, const fp8_kv_cache* cache,
+                        const int32_t* table, int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                        float scale, int64_t window, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp8_status_string(int status);
 
