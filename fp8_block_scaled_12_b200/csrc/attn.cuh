@@ -21,14 +21,16 @@
 //            most 2^-17 relative, or 2^-30 of the tile's largest possible w.  Each tile's
 //            product lands in fresh tensor-memory columns and is folded into fp32 registers
 //            (one channel d per thread) with the running maximum's factors.
-// A CTA (one per SM): warp 0 loads pages (TMA; one lane per box of gcd(page, 128) rows, its
-// scales by bulk copies), warp 1 issues MMAs, warps 2-5 do softmax and accumulation.
+// A CTA (one per SM): warps 0 and 3 load pages (TMA; one lane per box of gcd(page, 128) rows)
+// and scales, warp 1 issues the score MMAs, warp 2 the output MMAs, and two warpgroups (warps
+// 4-11) do softmax and accumulation.  Each warpgroup works through a range of
+// tiles of its own; the loads and MMAs take one tile of each in turn.
 //
 // Split: the batch's tiles, row after row (a row is a sequence, kv head and chunk of GT query
-// heads), form one list that is cut into equal ranges, one per CTA, whatever the lengths.
-// A row inside one range is finished there; a row cut by a border leaves partial sums (o, m, l)
-// in the workspace, which k_attn_join adds up in the order of the tiles, so results do not
-// depend on timing.
+// heads), form one list that is cut into equal ranges, one per warpgroup ("worker"), whatever
+// the lengths.  A row inside one range is finished there; a row cut by a border leaves partial
+// sums (o, m, l) in the workspace, which k_attn_join adds up in the order of the tiles, so
+// results do not depend on timing.
 //
 // Masked tokens (beyond the length, before the window, or of a page id outside the cache):
 // boxes without any valid token are zero-filled by TMA (an out-of-range page coordinate: no
@@ -42,13 +44,18 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "gemm.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
 namespace fp8lin {
 
-constexpr int kAttnThreads = 192;
+constexpr int kAttnThreads = 384;
 constexpr int kAttnTile = 128;
+// Register split of the variant with 16 heads (the pool is kLaunchRegs a thread).
+constexpr uint32_t kAttnLoadRegs = 88, kAttnSoftmaxRegs = 208;
+static_assert(128 * kAttnLoadRegs + 256 * kAttnSoftmaxRegs <= 384 * kLaunchRegs, "register split exceeds pool");
+static_assert(kAttnThreads == 384, "the split is of 384 threads");
 
 struct AttnArgs {
   const uint16_t* q;       // bf16 [B][Hq][D], strides below
@@ -58,9 +65,9 @@ struct AttnArgs {
   const int32_t* lens;     // [B]
   uint16_t* out;           // bf16 [B][Hq][D]
   float* lse;              // [B][Hq] or nullptr
-  float* ws_o;             // [2 * CTAs][GT][D]
-  float* ws_ml;            // [2 * CTAs][2][GT]
-  int2* ws_row;            // [rows]: (slot of the first partial, CTA of the last one), or (-1, -1)
+  float* ws_o;             // [2 * workers][GT][D]: a worker's first and last segment
+  float* ws_ml;            // [2 * workers][2][GT]
+  int2* ws_row;            // [rows]: (slot of the first partial, worker of the last), or (-1, -1)
   int64_t q_row, q_head, table_stride;
   int64_t window, cap;     // tokens; window 0 = none; cap = max_pages * P
   int64_t pages;
@@ -71,34 +78,37 @@ struct AttnArgs {
 template <int GT_, int DCH_>
 struct AttnCfg {
   static constexpr int GT = GT_, DCH = DCH_;
-  static constexpr int STAGES = DCH == 1 ? 6 : 3;
+  static constexpr int STAGES = DCH == 2 ? 3 : GT == 8 ? 6 : 5;
   static constexpr uint32_t KV_BYTES = kAttnTile * 128 * DCH;
   static constexpr uint32_t Q_BYTES = 2 * GT * 128 * DCH;
   static constexpr uint32_t P_ROW = 4 * GT;                  // bytes per token of the split weights
   static constexpr uint32_t P_BYTES = kAttnTile * P_ROW;
   static constexpr uint32_t OFF_Q = STAGES * 2 * KV_BYTES;
-  static constexpr uint32_t OFF_P = OFF_Q + 2 * Q_BYTES;
-  static constexpr uint32_t OFF_S = OFF_P + P_BYTES;         // scales: [STAGES][2][128] fp32
+  static constexpr uint32_t OFF_P = OFF_Q + 4 * Q_BYTES;     // queries: two buffers a warpgroup
+  static constexpr uint32_t OFF_S = OFF_P + 2 * P_BYTES;     // scales: [STAGES][2][128] fp32
   static constexpr uint32_t OFF_STATE = OFF_S + STAGES * 1024;
   static constexpr uint32_t S_COLS = 2 * GT, O_COLS = 4 * GT;
-  static constexpr uint32_t TMEM_USED = 2 * S_COLS + DCH * O_COLS;
+  static constexpr uint32_t TMEM_USED = 2 * (S_COLS + DCH * O_COLS);
   static constexpr uint32_t TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : 256;
 };
 
 template <int GT, int STAGES>
-struct alignas(16) AttnState {
-  float red[2][4][GT];     // per-warp maxima, double-buffered by tile
-  float redsv[2][4];
-  float lsum[4][GT];
-  float cq[2][GT];         // per-head factor of the staged queries
-  uint64_t full[STAGES];
+struct alignas(16) AttnState {            // arrays [2]: by warpgroup
+  float red[2][2][4][GT];  // [parity of its tile]: per-warp maxima
+  float redsv[2][2][4];
+  float lsum[2][4][GT];    // per-warp sums of p
+  float cq[2][2][GT];      // per-head factor of the staged queries
+  uint64_t full[STAGES];   // pages
+  uint64_t scales[STAGES];
   uint64_t empty[STAGES];
-  uint64_t sfull[2], qfull[2];
-  uint64_t pfull, ofull, drain;
+  uint64_t qfull[2][2];    // [buffer]
+  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t drain[2];
   uint32_t boxes[STAGES];  // which boxes of the stage hold a valid page
+  int seg[STAGES];         // its segment of the worker's range
   uint32_t tmem_base;
   int abort;
-  int total, first_b, first_off;
+  int total, first_b[2], first_off[2];
 };
 
 template <class C>
@@ -122,30 +132,46 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// The walk over a CTA's range of tiles, segment by segment (a segment: the part of one row
-// inside the range).  Every role walks the same sequence.
+// The ranges of the list of tiles: worker k of n takes [total k / n, total (k + 1) / n).  Workers
+// of one CTA are grid.x apart, so few tiles spread over the SMs first.
+struct AttnPlan {
+  int total, workers;
+  __device__ __forceinline__ AttnPlan(int total_) : total(total_), workers(min(2 * int(gridDim.x), total_)) {}
+  __device__ __forceinline__ int begin(int k) const { return int(int64_t(total) * min(k, workers) / workers); }
+  __device__ __forceinline__ int worker(int wg) const { return int(blockIdx.x) + wg * int(gridDim.x); }
+  __device__ __forceinline__ int count(int wg) const { return begin(worker(wg) + 1) - begin(worker(wg)); }
+};
+
+// Place in the CTA's sequence of loads of tile j of warpgroup g: the warpgroups take turns
+// while both have tiles.
+__device__ __forceinline__ int attn_place(int j, int g, int fewer) { return j < fewer ? 2 * j + g : j + fewer; }
+
+// The walk over a worker's range, tile by tile (next_tile) or segment by segment (a segment:
+// the part of one row inside the range).  Every role walks the same sequence.
 struct AttnWalk {
-  int b, rr, t0, t1, left;
+  int b, rr, t, t1, left;    // tiles [t, t1) of the segment are still to come, `left` after it
   AttnSeq s;
   __device__ __forceinline__ void start(const AttnArgs& a, int first_b, int off, int count) {
     b = first_b;
     s = attn_seq(a, b);
     rr = off / s.n;
-    t0 = off - rr * s.n;
-    t1 = min(s.n, t0 + count);
-    left = count - (t1 - t0);
+    t = off - rr * s.n;
+    t1 = min(s.n, t + count);
+    left = count - (t1 - t);
   }
-  __device__ __forceinline__ bool next(const AttnArgs& a) {
+  __device__ __forceinline__ bool next_segment(const AttnArgs& a) {
     if (left <= 0) return false;
     if (++rr == a.H * a.HC) {
       rr = 0;
       s = attn_seq(a, ++b);
     }
-    t0 = 0;
+    t = 0;
     t1 = min(s.n, left);
     left -= t1;
     return true;
   }
+  // to the next tile; true if it begins another segment
+  __device__ __forceinline__ bool next_tile(const AttnArgs& a) { return ++t == t1 && next_segment(a); }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -158,16 +184,24 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// Barrier of the 128 softmax threads that also tells whether any of them has failed.
-__device__ __forceinline__ bool attn_barrier_or(bool p) {
+// Barrier of `threads` threads that also tells whether any of them has failed.
+__device__ __forceinline__ bool attn_barrier_or(int id, int threads, bool p) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(int(p))
+      : "r"(int(p)), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
+}
+// 16-byte global -> shared copy that does not block the issuing thread, and the arrival on
+// `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -180,13 +214,23 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Shared-memory descriptor of an MN-major operand (rows along K, `row` bytes of the M or N
-// axis each, written with the swizzle of that width): 8-row groups `row * 8` bytes apart in
-// the stride offset; the leading offset is unused because one row spans the whole M or N.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t row) {
-  const uint64_t layout = row == 128 ? 2u : row == 64 ? 4u : 6u;    // 128-, 64-, 32-byte swizzle
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)((row * 8) >> 4) << 32) |
-         ((uint64_t)1 << 46) | (layout << 61);
+// Shared-memory descriptors.  K-major operands have rows of 128 bytes (the layout of
+// sw128_kmajor_desc); MN-major ones have rows along K that hold `row` bytes of the whole M or N,
+// written with the swizzle of that width.  Either way 8-row groups are row * 8 bytes apart
+// (stride offset) and the leading offset is unused.  The low word holds the address in units
+// of 16 bytes, so that steps are additions of constants to it.
+__device__ __forceinline__ uint32_t attn_desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t attn_desc(uint32_t lo, uint32_t row) {
+  const uint32_t layout = row == 128 ? 2u : row == 64 ? 4u : 6u;    // 128-, 64-, 32-byte swizzle
+  const uint32_t hi = ((row * 8) >> 4) | (1u << 14) | (layout << 29);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // Instruction descriptor with A in the cache's format (0 E4M3, 1 E5M2), B E4M3; `mn`: both
 // operands MN-major.
@@ -206,16 +250,17 @@ __device__ __forceinline__ uint32_t split16(float& a, float& b) {
 }
 
 // Scan of the batch by one warp: the number of tiles of all rows, then the sequence and the
-// offset in its rows at which this CTA's range begins.
-__device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int* total, int* first_b, int* first_off) {
+// offset in its rows at which the range of this CTA's warpgroup `wg` begins.
+__device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int wg, int* total, int* first_b,
+                                          int* first_off) {
   const int rows = a.H * a.HC;
   int sum = 0;
   for (int i = 0; i < a.B; i += 32)
     sum += __reduce_add_sync(~0u, i + lane < a.B ? attn_seq(a, i + lane).n * rows : 0);
-  const int ctas = min(int(gridDim.x), sum);
-  const int x0 = int(int64_t(sum) * blockIdx.x / ctas);
+  const AttnPlan plan(sum);
+  const int x0 = plan.begin(plan.worker(wg));
   int run = 0;
-  for (int i = 0; i < a.B; i += 32) {
+  for (int i = 0; i < a.B && run <= x0; i += 32) {
     const int v = i + lane < a.B ? attn_seq(a, i + lane).n * rows : 0;
     int inc = v;
 #pragma unroll
@@ -228,30 +273,33 @@ __device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int* tota
       *first_off = x0 - (run + inc - v);
     }
     run += __shfl_sync(~0u, inc, 31);
-    if (run > x0) break;
   }
   if (lane == 0) *total = sum;
 }
 
 // Queries of a segment -> two E4M3 pieces as K-major rows (hi: head g, lo: head GT + g) in
-// shared memory, and the factor that turns their products into base-2 exponents.
+// shared memory, and the factor that turns their products into base-2 exponents.  A thread
+// owns 16 channels of a head; loading and storing are apart, so that a tile's work hides the
+// loads' latency.
 template <class C>
-__device__ __forceinline__ void attn_stage_q(const AttnArgs& a, const AttnWalk& w, uint8_t* sq, float* cq, int tid) {
-  constexpr int UPH = 8 * C::DCH;            // 16-channel units per head
-  const int c = w.rr / a.HC, g0 = (w.rr % a.HC) * C::GT;
-#pragma unroll
-  for (int u0 = 0; u0 < C::GT * UPH; u0 += 128) {
-    const int u = u0 + tid;
-    const bool on = u < C::GT * UPH;         // uniform over a warp: units come in multiples of 64
-    if (!on) break;
-    const int head = u / UPH, ch = u % UPH;
-    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (g0 + head < a.G && ch * 16 < a.D) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(w.b) * a.q_row +
-                                                      int64_t(c * a.G + g0 + head) * a.q_head + ch * 16);
+struct AttnQuery {
+  static constexpr int UPH = 8 * C::DCH;     // units of 16 channels per head
+  static constexpr bool ALL = C::GT * UPH >= 128;
+  static_assert(C::GT * UPH <= 128, "one unit a thread");
+  uint4 v[2];
+  __device__ __forceinline__ void load(const AttnArgs& a, const AttnWalk& w, int tid) {
+    const int c = w.rr / a.HC, g = (w.rr - c * a.HC) * C::GT + tid / UPH, ch = tid % UPH;
+    v[0] = v[1] = make_uint4(0, 0, 0, 0);
+    if ((ALL || tid < C::GT * UPH) && g < a.G && ch * 16 < a.D) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(w.b) * a.q_row + int64_t(c * a.G + g) * a.q_head +
+                                                      ch * 16);
       v[0] = __ldg(p);
       v[1] = __ldg(p + 1);
     }
+  }
+  __device__ __forceinline__ void store(const AttnArgs& a, uint8_t* sq, float* cq, int tid) const {
+    if (!ALL && tid >= C::GT * UPH) return;  // uniform over a warp
+    const int head = tid / UPH, ch = tid % UPH;
     const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t mx = 0;                         // largest |q| as bf16 bits: NaN and Inf sort above all
 #pragma unroll
@@ -270,12 +318,28 @@ __device__ __forceinline__ void attn_stage_q(const AttnArgs& a, const AttnWalk& 
       hi[i] = bad ? 0x7F7F7F7Fu : h0 | (h1 << 16);
       lo[i] = bad ? 0x7F7F7F7Fu : cvt2<kE4M3>(p0, p1) | (cvt2<kE4M3>(p2, p3) << 16);
     }
-    uint8_t* base = sq + (ch / 8) * (2 * C::GT * 128);
-    *reinterpret_cast<uint4*>(base + head * 128 + (((ch & 7) ^ (head & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(base + (C::GT + head) * 128 + (((ch & 7) ^ (head & 7)) * 16)) =
-        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    uint8_t* base = sq + (ch / 8) * (2 * C::GT * 128) + (((ch & 7) ^ (head & 7)) * 16);
+    *reinterpret_cast<uint4*>(base + head * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(base + (C::GT + head) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (ch == 0) cq[head] = a.scale * 1.44269504088896340736f / up;
   }
+};
+
+// mbar_wait with the limit read once per kernel and a number of polls before the clock is
+// looked at: reading either costs more than most of this kernel's waits.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (limit_ns >= 1000) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  }
+  return mbar_wait(bar, parity, abort, limit_ns);
+}
+
+// The same by a whole warp, all of whose lanes get the same answer.
+__device__ __forceinline__ bool attn_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return __all_sync(~0u, attn_wait(bar, parity, abort, limit_ns));
 }
 
 template <int FMT, class C>
@@ -290,20 +354,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint8_t* gbase = smem_raw + (base - raw);
   State* ps = reinterpret_cast<State*>(gbase + C::OFF_STATE);
   volatile int* abort = &ps->abort;
+  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&ps->full[s]), 1);
+      mbar_init(smem_u32(&ps->scales[s]), 32);
       mbar_init(smem_u32(&ps->empty[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ps->qfull[i][0]), 4);
+      mbar_init(smem_u32(&ps->qfull[i][1]), 4);
       mbar_init(smem_u32(&ps->sfull[i]), 1);
-      mbar_init(smem_u32(&ps->qfull[i]), 4);
+      mbar_init(smem_u32(&ps->pfull[i]), 4);
+      mbar_init(smem_u32(&ps->ofull[i]), 1);
+      mbar_init(smem_u32(&ps->drain[i]), 1);
     }
-    mbar_init(smem_u32(&ps->pfull), 4);
-    mbar_init(smem_u32(&ps->ofull), 1);
-    mbar_init(smem_u32(&ps->drain), 1);
     ps->abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmK);
@@ -314,168 +381,216 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  if (warp == 2) attn_scan(a, lane, &ps->total, &ps->first_b, &ps->first_off);
+  if (warp == 2 || warp == 3) attn_scan(a, lane, warp - 2, &ps->total, &ps->first_b[warp - 2], &ps->first_off[warp - 2]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ps->tmem_base;
-  const uint32_t tmem_o = tmem + 2 * C::S_COLS;
-  const int total = ps->total;
-  const int ctas = min(int(gridDim.x), total);
-  const int cta = blockIdx.x;
-  const int count = cta < ctas ? int(int64_t(total) * (cta + 1) / ctas) - int(int64_t(total) * cta / ctas) : 0;
+  const uint32_t tmem = ps->tmem_base;                 // scores of both warpgroups, then outputs
+  const AttnPlan plan(ps->total);
+  const int n0 = plan.count(0), n1 = plan.count(1);
+  const int fewer = min(n0, n1), more = max(n0, n1);
 
-  if (count > 0) {
-    AttnWalk w;
-    w.start(a, ps->first_b, ps->first_off, count);
-    if (warp == 0) {
-      // ------------------------------------------------ pages -> shared memory
-      const int nb = kAttnTile / a.BR;
-      int t = w.t0;
-      // this lane's box of tile t: its page if it holds a token, and the row inside it
-      auto lookup = [&](int& page, int& row) {
-        const int tok = (w.s.ft + t) * kAttnTile + lane * a.BR;
-        page = -1;
-        row = 0;
-        if (lane < nb && tok < w.s.len && tok + a.BR > w.s.st) {
-          const int p = tok / a.P;
-          row = tok - p * a.P;
-          page = __ldg(a.table + int64_t(w.b) * a.table_stride + p);
-        }
-      };
-      int page, row;
-      lookup(page, row);
-      int it = 0;
-      for (; it < count; ++it) {
-        const int h = w.rr / a.HC;
-        const int pg = page, rw = row;
-        if (++t == w.t1 && w.next(a)) t = 0;
-        if (it + 1 < count) lookup(page, row);
-        const int s = it % STAGES;
-        if (!__all_sync(~0u, mbar_wait(smem_u32(&ps->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort))) break;
-        const bool ok = pg >= 0 && pg < a.pages;
-        const uint32_t bar = smem_u32(&ps->full[s]);
-        const uint32_t boxes = __ballot_sync(~0u, ok);
-        if (lane == 0) {
-          ps->boxes[s] = boxes;
-          mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES + __popc(boxes) * uint32_t(a.BR) * 8u);
-        }
-        __syncwarp();
-        if (lane < nb) {
-          const uint32_t off = base + uint32_t(s) * (2 * C::KV_BYTES) + uint32_t(lane * a.BR) * 128u;
-          const int pc = ok ? pg : int(a.pages);
+  // (8 heads fit the registers of an even split)
+  if (warp < 4) {
+    if constexpr (GT > 8) setmaxnreg_dec<kAttnLoadRegs>();
+    const int count = n0 + n1;
+    const int longer = n0 >= n1 ? 0 : 1;               // takes the tiles left when the turns are over
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------ pages and scales -> shared memory
+      // one warp for each warpgroup's tiles; a lane owns a box of the tile and the scales of
+      // four tokens (rows of a box come in multiples of eight)
+      const int g = warp == 0 ? 0 : 1, n = g == 0 ? n0 : n1;
+      int j = 0;
+      if (n > 0) {
+        AttnWalk w;
+        w.start(a, ps->first_b[g], ps->first_off[g], n);
+        const int nb = kAttnTile / a.BR;
+        const int sbox = lane * 4 / a.BR, srow = lane * 4 - sbox * a.BR;
+        const int step_p = kAttnTile / a.P, step_r = kAttnTile - step_p * a.P;   // a tile further in pages and rows
+        int seg = 0, h, tok, pi, row, page;
+        const int32_t* trow;
+        auto lookup = [&]() {              // the page of this lane's box, -1 if none of its tokens counts
+          page = -1;
+          if (lane < nb && tok < w.s.len && tok + a.BR > w.s.st) page = __ldg(trow + pi);
+        };
+        auto enter = [&]() {               // a segment's first tile
+          h = w.rr / a.HC;
+          tok = (w.s.ft + w.t) * kAttnTile + lane * a.BR;
+          pi = tok / a.P;
+          row = tok - pi * a.P;
+          trow = a.table + int64_t(w.b) * a.table_stride;
+          lookup();
+        };
+        enter();
+        for (; j < n; ++j) {
+          const int it = attn_place(j, g, fewer), s = it % STAGES;
+          const int pg = page, rw = row, ch = h, sg = seg;
+          if (j + 1 < n) {
+            if (w.next_tile(a)) {
+              ++seg;
+              enter();
+            } else {
+              tok += kAttnTile;
+              pi += step_p;
+              row += step_r;
+              if (row >= a.P) {
+                row -= a.P;
+                ++pi;
+              }
+              lookup();
+            }
+          }
+          if (!attn_wait_warp(smem_u32(&ps->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, limit)) break;
+          const bool ok = pg >= 0 && pg < a.pages;
+          const uint32_t bar = smem_u32(&ps->full[s]);
+          const uint32_t boxes = __ballot_sync(~0u, ok);
+          if (lane == 0) {
+            ps->boxes[s] = boxes;
+            ps->seg[s] = sg;
+            mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES);
+          }
+          __syncwarp();
+          if (lane < nb) {
+            const uint32_t off = base + uint32_t(s) * (2 * C::KV_BYTES) + uint32_t(lane * a.BR) * 128u;
+            const int pc = ok ? pg : int(a.pages);
 #pragma unroll
-          for (int c = 0; c < DCH; ++c) {
-            tma_load_4d(off + c * (kAttnTile * 128), &tmK, bar, c * 128, rw, h, pc);
-            tma_load_4d(off + C::KV_BYTES + c * (kAttnTile * 128), &tmV, bar, c * 128, rw, h, pc);
+            for (int c = 0; c < DCH; ++c) {
+              tma_load_4d(off + c * (kAttnTile * 128), &tmK, bar, c * 128, rw, ch, pc);
+              tma_load_4d(off + C::KV_BYTES + c * (kAttnTile * 128), &tmV, bar, c * 128, rw, ch, pc);
+            }
           }
-          if (ok) {
-            const int64_t at = (int64_t(pg) * a.H + h) * a.P + rw;
-            const uint32_t sc = base + C::OFF_S + s * 1024 + lane * a.BR * 4;
-            bulk_load(sc, a.ks + at, uint32_t(a.BR) * 4u, bar);
-            bulk_load(sc + 512, a.vs + at, uint32_t(a.BR) * 4u, bar);
+          const int64_t spage = __shfl_sync(~0u, pg, sbox);
+          const int sr = __shfl_sync(~0u, rw, sbox) + srow;
+          if ((boxes >> sbox) & 1u) {
+            const int64_t at = (spage * a.H + ch) * a.P + sr;
+            const uint32_t sc = base + C::OFF_S + s * 1024 + lane * 16;
+            cp_async16(sc, a.ks + at);
+            cp_async16(sc + 512, a.vs + at);
           }
+          cp_async_arrive(smem_u32(&ps->scales[s]));
         }
       }
       if (*abort) {                      // every load already issued lands before the CTA exits
-        for (int j = max(0, it - STAGES); j < it; ++j)
-          mbar_drain(smem_u32(&ps->full[j % STAGES]), (j / STAGES) & 1u);
+        for (int i = max(0, j - STAGES); i < j; ++i) {
+          const int it = attn_place(i, g, fewer);
+          mbar_drain(smem_u32(&ps->full[it % STAGES]), (it / STAGES) & 1u);
+        }
+        cp_async_wait_all();
       }
-      pdl_trigger();
+      if (warp == 0) pdl_trigger();
     } else if (warp == 1) {
-      if (lane == 0) {
-        // ---------------------------------------------- MMA issuer
-        constexpr uint32_t id_s = attn_idesc(FMT, 2 * GT, false), id_o = attn_idesc(FMT, 4 * GT, true);
-        int t = w.t0, seg = 0;
-        bool fresh = true;                 // the next tile is the first of its segment
-        auto scores = [&](int i) {         // S of tile i; tiles come in order
-          const int s = i % STAGES;
-          if (fresh && !mbar_wait(smem_u32(&ps->qfull[seg & 1]), (seg >> 1) & 1u, abort)) return false;
-          if (!mbar_wait(smem_u32(&ps->full[s]), (i / STAGES) & 1u, abort)) return false;
-          tc_fence_after();
-          const uint32_t k0 = base + uint32_t(s) * (2 * C::KV_BYTES);
-          const uint32_t q0 = base + C::OFF_Q + (seg & 1) * C::Q_BYTES;
+      // ------------------------------------------------ scores
+      // (the whole warp walks, one elected lane issues: operands then stay in uniform registers)
+      constexpr uint32_t id_s = attn_idesc(FMT, 2 * GT, false);
+      const int steps = (a.D + 31) / 32;
+      const uint32_t klo = attn_desc_lo(base), qlo = attn_desc_lo(base + C::OFF_Q);
+      for (int it = 0; it < count; ++it) {
+        const int s = it % STAGES;
+        const int g = it < 2 * fewer ? it & 1 : longer, j = it < 2 * fewer ? it >> 1 : it - fewer;
+        // the tile; the warpgroup's previous scores, taken before it announces its weights; the queries
+        if (!attn_wait_warp(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort, limit)) break;
+        if (j > 0 && !attn_wait_warp(smem_u32(&ps->pfull[g]), (j & 1u) ^ 1u, abort, limit)) break;
+        const int seg = ps->seg[s];
+        if (!attn_wait_warp(smem_u32(&ps->qfull[g][seg & 1]), (seg >> 1) & 1u, abort, limit)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t k0 = klo + uint32_t(s) * (2 * C::KV_BYTES / 16);
+          const uint32_t q0 = qlo + uint32_t(2 * g + (seg & 1)) * (C::Q_BYTES / 16);
 #pragma unroll
           for (int k = 0; k < 4 * DCH; ++k)
-            mma_f8(tmem + (i & 1) * C::S_COLS, sw128_kmajor_desc(k0 + (k / 4) * (kAttnTile * 128) + (k % 4) * 32),
-                   sw128_kmajor_desc(q0 + (k / 4) * (2 * GT * 128) + (k % 4) * 32), id_s, k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&ps->sfull[i & 1]));
-          fresh = false;
-          if (++t == w.t1 && w.next(a)) {
-            t = 0;
-            ++seg;
-            fresh = true;
-          }
-          return true;
-        };
-        bool ok = scores(0) && (count < 2 || scores(1));
-        for (int i = 0; ok && i < count; ++i) {
-          if (!mbar_wait(smem_u32(&ps->pfull), i & 1u, abort)) break;
-          tc_fence_after();
-          const int s = i % STAGES;
-          const uint32_t v0 = base + uint32_t(s) * (2 * C::KV_BYTES) + C::KV_BYTES;
+            if (k < steps)
+              mma_f8(tmem + g * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
+                     attn_desc(q0 + (k / 4) * (2 * GT * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&ps->sfull[g]));
+        }
+        __syncwarp();
+      }
+      if (*abort && lane == 0) {           // the MMAs already issued finish before tensor memory is freed
+        mma_commit(smem_u32(&ps->drain[0]));
+        mbar_drain(smem_u32(&ps->drain[0]), 0u);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------ outputs
+      constexpr uint32_t id_o = attn_idesc(FMT, 4 * GT, true);
+      const uint32_t vlo = attn_desc_lo(base + C::KV_BYTES), plo = attn_desc_lo(base + C::OFF_P);
+      for (int it = 0; it < count; ++it) {
+        const int s = it % STAGES;
+        const int g = it < 2 * fewer ? it & 1 : longer, j = it < 2 * fewer ? it >> 1 : it - fewer;
+        if (!attn_wait_warp(smem_u32(&ps->pfull[g]), j & 1u, abort, limit)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v0 = vlo + uint32_t(s) * (2 * C::KV_BYTES / 16);
+          const uint32_t p0 = plo + uint32_t(g) * (C::P_BYTES / 16);
+          const uint32_t o0 = tmem + 2 * C::S_COLS + g * (DCH * C::O_COLS);
 #pragma unroll
           for (int c = 0; c < DCH; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8(tmem_o + c * C::O_COLS, mn_desc(v0 + c * (kAttnTile * 128) + k * 32 * 128, 128),
-                     mn_desc(base + C::OFF_P + k * 32 * C::P_ROW, C::P_ROW), id_o, k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&ps->ofull));
+              mma_f8(o0 + c * C::O_COLS, attn_desc(v0 + c * (kAttnTile * 8) + k * (32 * 8), 128),
+                     attn_desc(p0 + k * (2 * C::P_ROW), C::P_ROW), id_o, k > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&ps->ofull[g]));
           mma_commit(smem_u32(&ps->empty[s]));
-          if (i + 2 < count) ok = scores(i + 2);
         }
-        if (*abort) {                      // the MMAs already issued finish before tensor memory is freed
-          mma_commit(smem_u32(&ps->drain));
-          mbar_drain(smem_u32(&ps->drain), 0u);
-        }
+        __syncwarp();
       }
-    } else {
+      if (*abort && lane == 0) {
+        mma_commit(smem_u32(&ps->drain[1]));
+        mbar_drain(smem_u32(&ps->drain[1]), 0u);
+      }
+    }
+  } else {
+    if constexpr (GT > 8) setmaxnreg_inc<kAttnSoftmaxRegs>();
+    const int wg = (warp - 4) >> 2;
+    const int mine = wg == 0 ? n0 : n1;
+    if (mine > 0) {
       // ------------------------------------------------ softmax and accumulation
-      const int tid = threadIdx.x - 64;            // staging unit and barrier index
       const int quad = warp & 3;                   // tensor-memory lanes of this warp
       const int tok = quad * 32 + lane;            // token of the tile; channel of the output
       const uint32_t tlane = uint32_t(quad * 32) << 16;
-      uint8_t* sq = gbase + C::OFF_Q;
-      auto stage = [&](const AttnWalk& x, int buf) {
-        attn_stage_q<C>(a, x, sq + buf * C::Q_BYTES, ps->cq[buf], tid);
+      const uint32_t tmem_s = tmem + tlane + wg * C::S_COLS;
+      const uint32_t tmem_o = tmem + tlane + 2 * C::S_COLS + wg * (DCH * C::O_COLS);
+      const int worker = plan.worker(wg);
+      AttnWalk w;
+      w.start(a, ps->first_b[wg], ps->first_off[wg], mine);
+      AttnWalk ahead = w;                          // the next segment whose queries are staged
+      AttnQuery<C> qn;
+      auto stage = [&](int buf) {
+        qn.store(a, gbase + C::OFF_Q + (2 * wg + buf) * C::Q_BYTES, ps->cq[wg][buf], tok);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ps->qfull[buf]));
+        if (lane == 0) mbar_arrive(smem_u32(&ps->qfull[wg][buf]));
       };
-      AttnWalk ahead = w;                          // the segment whose queries are staged next
-      stage(ahead, 0);
-      bool more = ahead.next(a);
+      qn.load(a, ahead, tok);
+      stage(0);
       bool ok = true;
-      attn_barrier_or(false);                      // the first segment's factors are visible
-      int it = 0;
+      attn_barrier_or(1 + wg, 128, false);         // the first segment's factors are visible
+      int j = 0;                                   // this warpgroup's tile
       for (int seg = 0;; ++seg) {
-        if (more) {                                // the buffer's last reader, segment seg - 1, is done
-          stage(ahead, (seg + 1) & 1);
-          more = ahead.next(a);
-        }
+        bool staging = ahead.next_segment(a);
+        if (staging) qn.load(a, ahead, tok);
         float cq[GT], m[GT], l[GT], o[DCH][GT], fa[GT], fb[GT];
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-          cq[g] = ps->cq[seg & 1][g];
+          cq[g] = ps->cq[wg][seg & 1][g];
           m[g] = -INFINITY;
           l[g] = 0.0f;
           fa[g] = fb[g] = 0.0f;
 #pragma unroll
           for (int c = 0; c < DCH; ++c) o[c][g] = 0.0f;
         }
-        // o = o * fa + (product of the last tile) * fb
-        auto accumulate = [&](int i) {
-          ok &= mbar_wait(smem_u32(&ps->ofull), i & 1u, abort);
+        // o = o * fa + (product of this warpgroup's tile j) * fb
+        auto accumulate = [&](int j_) {
+          ok &= attn_wait(smem_u32(&ps->ofull[wg]), j_ & 1u, abort, limit);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < DCH; ++c) {
             uint32_t r[2][2 * GT];
             if constexpr (GT == 8) {
-              tmem_ld16(tmem_o + tlane + c * C::O_COLS, r[0]);
-              tmem_ld16(tmem_o + tlane + c * C::O_COLS + 16, r[1]);
+              tmem_ld16(tmem_o + c * C::O_COLS, r[0]);
+              tmem_ld16(tmem_o + c * C::O_COLS + 16, r[1]);
             } else {
-              tmem_ld32(tmem_o + tlane + c * C::O_COLS, r[0]);
-              tmem_ld32(tmem_o + tlane + c * C::O_COLS + 32, r[1]);
+              tmem_ld32(tmem_o + c * C::O_COLS, r[0]);
+              tmem_ld32(tmem_o + c * C::O_COLS + 32, r[1]);
             }
             tmem_ld_wait();
             tmem_regs_ready(r[0]);
@@ -488,142 +603,151 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         };
+        const int t_first = w.t;
         bool failed = false;
-        for (int t = w.t0; t < w.t1; ++t, ++it) {
-          const int s = it % STAGES, sb = it & 1;
-          ok &= mbar_wait(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort);
+        for (int t = t_first; t < w.t1; ++t, ++j) {
+          const int it = attn_place(j, wg, fewer), s = it % STAGES, par = j & 1;
+          ok &= attn_wait(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort, limit);
+          ok &= attn_wait(smem_u32(&ps->scales[s]), (it / STAGES) & 1u, abort, limit);
           const float* sc = reinterpret_cast<const float*>(gbase + C::OFF_S + s * 1024);
           const int t0 = (w.s.ft + t) * kAttnTile;
           const uint32_t boxes = ps->boxes[s];
           const bool live = t0 + tok >= w.s.st && t0 + tok < w.s.len && ((boxes >> (tok / a.BR)) & 1u);
           const float sk = live ? sc[tok] : 0.0f, sv = live ? sc[128 + tok] : 0.0f;
-          ok &= mbar_wait(smem_u32(&ps->sfull[sb]), (it >> 1) & 1u, abort);
+          ok &= attn_wait(smem_u32(&ps->sfull[wg]), par, abort, limit);
           tc_fence_after();
-          uint32_t r[2 * GT];
-          if constexpr (GT == 8) tmem_ld16(tmem + tlane + sb * C::S_COLS, r);
-          else tmem_ld32(tmem + tlane + sb * C::S_COLS, r);
-          tmem_ld_wait();
-          tmem_regs_ready(r);
           float x[GT];
+          {
+            uint32_t r[2 * GT];
+            if constexpr (GT == 8) tmem_ld16(tmem_s, r);
+            else tmem_ld32(tmem_s, r);
+            tmem_ld_wait();
+            tmem_regs_ready(r);
 #pragma unroll
-          for (int g = 0; g < GT; ++g) {
-            const float v = fmaf(__uint_as_float(r[GT + g]), 0.0625f, __uint_as_float(r[g])) * (cq[g] * sk);
-            x[g] = live ? v : -INFINITY;
-            const float wm = warp_max(x[g]);
-            if (lane == 0) ps->red[sb][quad][g] = wm;
+            for (int g = 0; g < GT; ++g) {
+              const float v = fmaf(__uint_as_float(r[GT + g]), 0.0625f, __uint_as_float(r[g])) * (cq[g] * sk);
+              x[g] = live ? v : -INFINITY;
+              const float wm = warp_max(x[g]);
+              if (lane == 0) ps->red[wg][par][quad][g] = wm;
+            }
           }
           {
             const float wm = warp_max(sv);
-            if (lane == 0) ps->redsv[sb][quad] = wm;
+            if (lane == 0) ps->redsv[wg][par][quad] = wm;
           }
-          if (attn_barrier_or(!ok)) {
+          if (t > t_first) accumulate(j - 1);
+          if (attn_barrier_or(1 + wg, 128, !ok)) {
             failed = true;
             break;
           }
-          const float4 vm = *reinterpret_cast<const float4*>(ps->redsv[sb]);
+          const float4 vm = *reinterpret_cast<const float4*>(ps->redsv[wg][par]);
           // 2^E >= the largest sv (E >= -110: below that, values are tiny against any other)
           const int E = max(int(__float_as_uint(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))) >> 23) - 126, -110);
           const float rsv = sv * __uint_as_float(uint32_t(8 - E + 127) << 23);
           const float down = __uint_as_float(uint32_t(E - 8 + 127) << 23);
-          float na[GT], nb[GT];
 #pragma unroll
           for (int g = 0; g < GT; ++g) {
-            const float tm = fmaxf(fmaxf(ps->red[sb][0][g], ps->red[sb][1][g]),
-                                   fmaxf(ps->red[sb][2][g], ps->red[sb][3][g]));
+            const float tm = fmaxf(fmaxf(ps->red[wg][par][0][g], ps->red[wg][par][1][g]),
+                                   fmaxf(ps->red[wg][par][2][g], ps->red[wg][par][3][g]));
             const float mn = fmaxf(m[g], tm);
             const float ref = mn == -INFINITY ? 0.0f : mn;      // nothing valid so far: every factor is 0
-            na[g] = ex2(m[g] - ref);
+            fa[g] = ex2(m[g] - ref);
             const float be = ex2(tm - ref);
             const float p = ex2(x[g] - (tm == -INFINITY ? 0.0f : tm));
             m[g] = mn;
-            l[g] = fmaf(l[g], na[g], p * be);
-            nb[g] = be * down;
+            l[g] = fmaf(l[g], fa[g], p * be);
+            fb[g] = be * down;
             x[g] = p * rsv;
           }
           uint32_t pk[GT];                                      // [piece][heads], 4 codes a word
 #pragma unroll
-          for (int j = 0; j < 3; ++j)
+          for (int i = 0; i < 3; ++i)
 #pragma unroll
             for (int g = 0; g < GT; g += 4)
-              pk[j * (GT / 4) + g / 4] = split16(x[g], x[g + 1]) | (split16(x[g + 2], x[g + 3]) << 16);
+              pk[i * (GT / 4) + g / 4] = split16(x[g], x[g + 1]) | (split16(x[g + 2], x[g + 3]) << 16);
 #pragma unroll
           for (int g = 0; g < GT; g += 4)
             pk[3 * (GT / 4) + g / 4] = cvt2<kE4M3>(x[g], x[g + 1]) | (cvt2<kE4M3>(x[g + 2], x[g + 3]) << 16);
-          if (t > w.t0) accumulate(it - 1);
-#pragma unroll
-          for (int g = 0; g < GT; ++g) {
-            fa[g] = na[g];
-            fb[g] = nb[g];
-          }
-          uint8_t* pr = gbase + C::OFF_P + tok * C::P_ROW;
+          uint8_t* pr = gbase + C::OFF_P + wg * C::P_BYTES + tok * C::P_ROW;
           const int sw = GT == 8 ? (tok >> 2) & 1 : (tok >> 1) & 3;
 #pragma unroll
-          for (int j = 0; j < GT / 4; ++j)
-            *reinterpret_cast<uint4*>(pr + ((j ^ sw) * 16)) =
-                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          for (int i = 0; i < GT / 4; ++i)
+            *reinterpret_cast<uint4*>(pr + ((i ^ sw) * 16)) =
+                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           if (!live) {                                          // whatever the cache holds there times 0 is 0
             uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(s) * (2 * C::KV_BYTES) + C::KV_BYTES + tok * 128);
 #pragma unroll
             for (int c = 0; c < DCH; ++c)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) vr[c * (kAttnTile * 8) + j] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < 8; ++i) vr[c * (kAttnTile * 8) + (i ^ (tok & 7))] = make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ps->pfull));
+          if (lane == 0) mbar_arrive(smem_u32(&ps->pfull[wg]));
+          if (staging) {                           // that buffer's reader, segment seg - 1, is done
+            stage((seg + 1) & 1);
+            staging = false;
+          }
         }
         if (failed) break;
-        accumulate(it - 1);
-        // sums of p over the tile's tokens
+        accumulate(j - 1);
+        // sums of p over the tokens
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) l[g] += __shfl_xor_sync(~0u, l[g], d);
-          if (lane == 0) ps->lsum[quad][g] = l[g];
+          if (lane == 0) ps->lsum[wg][quad][g] = l[g];
         }
-        if (attn_barrier_or(!ok)) break;
-        const int c = w.rr / a.HC, g0 = (w.rr % a.HC) * GT;
-        const int64_t row = int64_t(w.b) * (a.H * a.HC) + w.rr;
-        const bool whole = w.t0 == 0 && w.t1 == w.s.n;
-        const int slot = 2 * cta + (seg > 0 ? 1 : 0);
+        if (attn_barrier_or(1 + wg, 128, !ok)) break;
+        const int c = w.rr / a.HC, g0 = (w.rr - c * a.HC) * GT;
+        const bool whole = t_first == 0 && w.t1 == w.s.n;
+        const int heads = min(GT, a.G - g0);
+        const int64_t head0 = int64_t(w.b) * (int64_t(a.H) * a.G) + int64_t(c) * a.G + g0;
+        const int slot = 2 * worker + (seg > 0 ? 1 : 0);
+        // lane g: the sum of head g, for the warp
+        const int hg = lane < GT ? lane : 0;
+        const float sum = (ps->lsum[wg][0][hg] + ps->lsum[wg][1][hg]) + (ps->lsum[wg][2][hg] + ps->lsum[wg][3][hg]);
+        const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;     // no valid token: zeros
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-          const float sum = ps->lsum[0][g] + ps->lsum[1][g] + ps->lsum[2][g] + ps->lsum[3][g];
-          if (g0 + g < a.G) {
-            if (whole) {
-              const int64_t head = int64_t(w.b) * (int64_t(a.H) * a.G) + int64_t(c) * a.G + g0 + g;
-              const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;      // no valid token: zeros, lse -inf
+          if (g < heads && tok == g) {
+            if (!whole) {
+              a.ws_ml[(int64_t(slot) * 2) * GT + g] = m[g];
+              a.ws_ml[(int64_t(slot) * 2 + 1) * GT + g] = sum;
+            } else if (a.lse != nullptr) {
+              a.lse[head0 + g] = sum == 0.0f ? -INFINITY : (m[g] + __log2f(sum)) * 0.69314718055994530942f;
+            }
+          }
+          const float f = __shfl_sync(~0u, inv, g);
 #pragma unroll
-              for (int ch = 0; ch < DCH; ++ch)
-                if (ch * 128 + tok < a.D)
-                  reinterpret_cast<__nv_bfloat16*>(a.out)[head * a.D + ch * 128 + tok] =
-                      __float2bfloat16_rn(sum == 0.0f ? 0.0f : o[ch][g] * inv);
-              if (a.lse != nullptr && tok == g)
-                a.lse[head] = sum == 0.0f ? -INFINITY : (m[g] + __log2f(sum)) * 0.69314718055994530942f;
-            } else {
+          for (int ch = 0; ch < DCH; ++ch) o[ch][g] *= f;
+        }
 #pragma unroll
-              for (int ch = 0; ch < DCH; ++ch)
-                if (ch * 128 + tok < a.D)
-                  a.ws_o[(int64_t(slot) * GT + g) * a.D + ch * 128 + tok] = o[ch][g];
-              if (tok == g) {
-                a.ws_ml[(int64_t(slot) * 2) * GT + g] = m[g];
-                a.ws_ml[(int64_t(slot) * 2 + 1) * GT + g] = sum;
+        for (int ch = 0; ch < DCH; ++ch) {
+          if (ch * 128 + tok < a.D) {
+            __nv_bfloat16* po = reinterpret_cast<__nv_bfloat16*>(a.out) + head0 * a.D + ch * 128 + tok;
+            float* pw = a.ws_o + int64_t(slot) * GT * a.D + ch * 128 + tok;
+#pragma unroll
+            for (int g = 0; g < GT; ++g) {
+              if (g < heads) {
+                if (whole) po[g * a.D] = __float2bfloat16_rn(o[ch][g]);
+                else pw[g * a.D] = o[ch][g];
               }
             }
           }
         }
-        if (w.t0 == 0 && tok == 0) {
-          // the row's last tile in the list of all tiles, and the CTA whose range holds it
-          const int64_t last = int64_t(total) * cta / ctas + (it - (w.t1 - w.t0)) + w.s.n - 1;
-          const int lc = int(((last + 1) * ctas + total - 1) / total) - 1;
-          a.ws_row[row] = whole ? make_int2(-1, -1) : make_int2(slot, lc);
+        if (t_first == 0 && tok == 0) {
+          int2 info = make_int2(-1, -1);
+          if (!whole) {                            // the worker whose range holds the row's last tile
+            const int64_t last = int64_t(plan.begin(worker)) + j - w.t1 + w.s.n - 1;
+            info = make_int2(slot, int(((last + 1) * plan.workers + plan.total - 1) / plan.total) - 1);
+          }
+          a.ws_row[int64_t(w.b) * (a.H * a.HC) + w.rr] = info;
         }
-        if (!w.next(a)) break;
+        if (!w.next_segment(a)) break;
       }
     }
-  } else {
-    if (warp == 0) pdl_trigger();
   }
   tc_fence_before();
   __syncthreads();
@@ -631,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// Rows that more than one CTA worked on: their partial sums added up in the order of the
+// Rows that more than one worker has a part of: their partial sums added up in the order of the
 // tiles.  One block per row and head; its warps take the partials in turn.
 template <int GT>
 __global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a) {

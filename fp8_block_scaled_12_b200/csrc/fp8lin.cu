@@ -131,14 +131,14 @@ bool launch_regs_ok(K kern) {
 // The register check and the dynamic shared-memory limit of a warp-specialised kernel
 // persist in the device's context, so they run on its first launch per device only
 // (`ready`: one bit per device, owned by the calling launch function; devices past 63
-// are set up on every launch).
-template <typename K>
+// are set up on every launch).  SPLIT: whether the kernel splits its registers.
+template <bool SPLIT = true, typename K>
 int kernel_setup(std::atomic<uint64_t>& ready, K kern, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0u;
   if (bit != 0u && (ready.load(std::memory_order_acquire) & bit) != 0u) return FP8_OK;
-  if (!launch_regs_ok(kern)) return FP8_ERR_UNSUPPORTED;
+  if (SPLIT && !launch_regs_ok(kern)) return FP8_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return FP8_ERR_CUDA;
   ready.fetch_or(bit, std::memory_order_acq_rel);
@@ -366,19 +366,21 @@ bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t
   return r == CUDA_SUCCESS;
 }
 
-// Query heads of one kv head that a tile carries: 8, or 16 when a kv head has more.
-inline int attn_gt(int64_t G) { return G <= 8 ? 8 : 16; }
-inline int64_t attn_chunks(int64_t G) { return (G + attn_gt(G) - 1) / attn_gt(G); }
+// Query heads of one kv head that a tile carries: 8, or 16 when a kv head has more (at most
+// 8 for heads of over 128 channels, whose tiles leave no shared memory for more).
+inline int attn_gt(int64_t G, int64_t D) { return G <= 8 || D > 128 ? 8 : 16; }
+inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1) / attn_gt(G, D); }
 
-// Workspace of the attention: two partial sums per CTA, then one entry per row.
+// Workspace of the attention: two partial sums for each of two workers an SM, then one entry
+// per row.
 struct AttnWs {
   int64_t o, ml, row, total;
   AttnWs(int64_t B, int64_t H, int64_t G, int64_t D) {
-    const int64_t slots = 2 * int64_t(num_sms()), gt = attn_gt(G);
+    const int64_t slots = 4 * int64_t(num_sms()), gt = attn_gt(G, D);
     o = 0;
     ml = o + slots * gt * D * 4;
     row = ml + slots * 2 * gt * 4;
-    total = row + B * H * attn_chunks(G) * 8;
+    total = row + B * H * attn_chunks(G, D) * 8;
   }
 };
 
@@ -389,14 +391,7 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
   static_assert(smem <= 232448, "dynamic shared memory of one CTA (227 KB)");
   auto kern = k_paged_attention<FMT, C>;
   static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
-  const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0u;
-  if (bit == 0u || (ready.load(std::memory_order_acquire) & bit) == 0u) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-      return FP8_ERR_CUDA;
-    ready.fetch_or(bit, std::memory_order_acq_rel);
-  }
+  if (const int st_ = kernel_setup<(GT > 8)>(ready, kern, smem)) return st_;
   if (launch(kern, unsigned(grid), kAttnThreads, smem, st, mk, mv, a) != cudaSuccess) return FP8_ERR_CUDA;
   const int heads = a.G < GT ? a.G : GT;
   return cuda_status(launch(k_attn_join<GT>, dim3(unsigned(int64_t(a.B) * a.H * a.HC), unsigned(heads)), 128, 0, st, a));
@@ -404,9 +399,9 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
 
 template <int FMT>
 int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t st) {
-  if (attn_gt(a.G) == 8)
-    return a.D <= 128 ? launch_attention<FMT, 8, 1>(mk, mv, a, grid, st) : launch_attention<FMT, 8, 2>(mk, mv, a, grid, st);
-  return a.D <= 128 ? launch_attention<FMT, 16, 1>(mk, mv, a, grid, st) : launch_attention<FMT, 16, 2>(mk, mv, a, grid, st);
+  if (a.D > 128) return launch_attention<FMT, 8, 2>(mk, mv, a, grid, st);
+  return attn_gt(a.G, a.D) == 8 ? launch_attention<FMT, 8, 1>(mk, mv, a, grid, st)
+                                : launch_attention<FMT, 16, 1>(mk, mv, a, grid, st);
 }
 
 // Checks of a cache that every call shares.
@@ -904,7 +899,7 @@ int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B,
   if (int rc = check_cache(cache)) return rc;
   const int64_t H = cache->heads, D = cache->head_dim, P = cache->page_size;
   if (Hq % H != 0) return FP8_ERR_SHAPE;
-  const int64_t G = Hq / H, HC = attn_chunks(G);
+  const int64_t G = Hq / H, HC = attn_chunks(G, D);
   if (B > INT32_MAX || Hq > 65535 || B * H * HC > INT32_MAX) return FP8_ERR_SHAPE;
   if (max_pages > INT32_MAX / P || max_pages * P > INT32_MAX - 2 * kAttnTile) return FP8_ERR_SHAPE;
   const int64_t tiles = B * H * HC * ((max_pages * P + kAttnTile - 1) / kAttnTile + 1);
