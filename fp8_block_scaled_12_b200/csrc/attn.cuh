@@ -88,7 +88,7 @@ struct AttnCfg {
   static constexpr uint32_t OFF_S = OFF_P + 2 * P_BYTES;     // scales: [STAGES][2][128] fp32
   static constexpr uint32_t OFF_STATE = OFF_S + STAGES * 1024;
   static constexpr uint32_t S_COLS = 2 * GT, O_COLS = 4 * GT;
-  static constexpr uint32_t TMEM_USED = 2 * (S_COLS + DCH * O_COLS);
+  static constexpr uint32_t TMEM_USED = 2 * (2 * S_COLS + DCH * O_COLS);     // two score buffers a warpgroup
   static constexpr uint32_t TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : 256;
 };
 
@@ -102,7 +102,8 @@ struct alignas(16) AttnState {            // arrays [2]: by warpgroup
   uint64_t scales[STAGES];
   uint64_t empty[STAGES];
   uint64_t qfull[2][2];    // [buffer]
-  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t sfull[2][2], sfree[2][2];       // [parity of its tile]
+  uint64_t pfull[2], ofull[2];
   uint64_t drain[2];
   uint32_t boxes[STAGES];  // which boxes of the stage hold a valid page
   int seg[STAGES];         // its segment of the worker's range
@@ -149,21 +150,27 @@ __device__ __forceinline__ int attn_place(int j, int g, int fewer) { return j < 
 // The walk over a worker's range, tile by tile (next_tile) or segment by segment (a segment:
 // the part of one row inside the range).  Every role walks the same sequence.
 struct AttnWalk {
-  int b, rr, t, t1, left;    // tiles [t, t1) of the segment are still to come, `left` after it
+  int b, c, hc;              // the row: sequence, kv head, chunk of query heads
+  int t, t1, left;           // tiles [t, t1) of the segment are still to come, `left` after it
   AttnSeq s;
   __device__ __forceinline__ void start(const AttnArgs& a, int first_b, int off, int count) {
     b = first_b;
     s = attn_seq(a, b);
-    rr = off / s.n;
+    const int rr = off / s.n;
+    c = rr / a.HC;
+    hc = rr - c * a.HC;
     t = off - rr * s.n;
     t1 = min(s.n, t + count);
     left = count - (t1 - t);
   }
   __device__ __forceinline__ bool next_segment(const AttnArgs& a) {
     if (left <= 0) return false;
-    if (++rr == a.H * a.HC) {
-      rr = 0;
-      s = attn_seq(a, ++b);
+    if (++hc == a.HC) {
+      hc = 0;
+      if (++c == a.H) {
+        c = 0;
+        s = attn_seq(a, ++b);
+      }
     }
     t = 0;
     t1 = min(s.n, left);
@@ -173,6 +180,34 @@ struct AttnWalk {
   // to the next tile; true if it begins another segment
   __device__ __forceinline__ bool next_tile(const AttnArgs& a) { return ++t == t1 && next_segment(a); }
 };
+
+// Sums over the warp of N values a lane, N a power of two: in each step a lane passes half of
+// them on and adds what it gets to the other half.  Lane i returns the sum of value
+// i / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+  float r = v[0];
+  int d = 16;
+  if constexpr (N > 1) {
+    float h[N / 2];
+    const bool up = (lane & 16) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      h[i] = (up ? v[N / 2 + i] : v[i]) + __shfl_xor_sync(~0u, up ? v[i] : v[N / 2 + i], 16);
+    // the same with the next lower bit of the lane in the place of this one
+    int n = N / 2;
+    for (d = 8; n > 1; d >>= 1) {
+      n >>= 1;
+      const bool u = (lane & d) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i)
+        if (i < n) h[i] = (u ? h[n + i] : h[i]) + __shfl_xor_sync(~0u, u ? h[i] : h[n + i], d);
+    }
+    r = h[0];
+  }
+  for (; d > 0; d >>= 1) r += __shfl_xor_sync(~0u, r, d);
+  return r;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -195,11 +230,7 @@ __device__ __forceinline__ bool attn_barrier_or(int id, int threads, bool p) {
       : "memory");
   return r != 0;
 }
-// 16-byte global -> shared copy that does not block the issuing thread, and the arrival on
-// `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
+// Arrival on `bar` once this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -238,14 +269,15 @@ __device__ __forceinline__ constexpr uint32_t attn_idesc(int fmt, uint32_t n, bo
   return idesc_f8_e4m3_f32(128, n) | (uint32_t(fmt) << 7) | (mn ? (3u << 15) : 0u);
 }
 
-// fp32 pair -> two E4M3 codes and what they leave, times 16.
+// fp32 pair -> two E4M3 codes and what they leave, times 16 (exact).
 __device__ __forceinline__ uint32_t split16(float& a, float& b) {
   const uint32_t c = cvt2<kE4M3>(a, b);
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(c)));
   const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-  a = (a - f.x) * 16.0f;
-  b = (b - f.y) * 16.0f;
+  const float2 o = unpack2(fma2(pack2(f.x, f.y), pack2(-16.0f, -16.0f), mul2(pack2(a, b), pack2(16.0f, 16.0f))));
+  a = o.x;
+  b = o.y;
   return c;
 }
 
@@ -279,48 +311,61 @@ __device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int wg, i
 
 // Queries of a segment -> two E4M3 pieces as K-major rows (hi: head g, lo: head GT + g) in
 // shared memory, and the factor that turns their products into base-2 exponents.  A thread
-// owns 16 channels of a head; loading and storing are apart, so that a tile's work hides the
+// owns 8 or 16 channels of a head; loading and storing are apart, so that a tile's work hides the
 // loads' latency.
 template <class C>
 struct AttnQuery {
-  static constexpr int UPH = 8 * C::DCH;     // units of 16 channels per head
-  static constexpr bool ALL = C::GT * UPH >= 128;
-  static_assert(C::GT * UPH <= 128, "one unit a thread");
-  uint4 v[2];
+  static constexpr int UNIT = C::GT * C::DCH / 8 * 8;        // 128 threads share GT heads of 128 DCH channels
+  static constexpr int UPH = 128 * C::DCH / UNIT;            // units per head
+  static_assert(C::GT * UPH == 128 && (UNIT == 8 || UNIT == 16), "one unit a thread");
+  uint4 v[UNIT / 8];
   __device__ __forceinline__ void load(const AttnArgs& a, const AttnWalk& w, int tid) {
-    const int c = w.rr / a.HC, g = (w.rr - c * a.HC) * C::GT + tid / UPH, ch = tid % UPH;
-    v[0] = v[1] = make_uint4(0, 0, 0, 0);
-    if ((ALL || tid < C::GT * UPH) && g < a.G && ch * 16 < a.D) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(w.b) * a.q_row + int64_t(c * a.G + g) * a.q_head +
-                                                      ch * 16);
-      v[0] = __ldg(p);
-      v[1] = __ldg(p + 1);
+    const int g = w.hc * C::GT + tid / UPH, ch = tid % UPH * UNIT;
+#pragma unroll
+    for (int i = 0; i < UNIT / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    if (g < a.G && ch < a.D) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(w.b) * a.q_row + int64_t(w.c * a.G + g) * a.q_head +
+                                                      ch);
+#pragma unroll
+      for (int i = 0; i < UNIT / 8; ++i) v[i] = __ldg(p + i);
     }
   }
   __device__ __forceinline__ void store(const AttnArgs& a, uint8_t* sq, float* cq, int tid) const {
-    if (!ALL && tid >= C::GT * UPH) return;  // uniform over a warp
-    const int head = tid / UPH, ch = tid % UPH;
-    const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    const int head = tid / UPH, ch = tid % UPH * UNIT;
+    uint32_t x[UNIT / 2];
+#pragma unroll
+    for (int i = 0; i < UNIT / 8; ++i) {
+      x[4 * i] = v[i].x;
+      x[4 * i + 1] = v[i].y;
+      x[4 * i + 2] = v[i].z;
+      x[4 * i + 3] = v[i].w;
+    }
     uint32_t mx = 0;                         // largest |q| as bf16 bits: NaN and Inf sort above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = max(mx, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+    for (int i = 0; i < UNIT / 2; ++i) mx = max(mx, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
 #pragma unroll
     for (int d = 1; d < UPH; d <<= 1) mx = max(mx, __shfl_xor_sync(~0u, mx, d));
     const bool bad = mx >= 0x7F80u;          // a NaN or infinity: the head's output is NaN
     const int e = min(7 - (int(mx >> 7) - 127), 126);       // q 2^e in [128, 256)
     const float up = __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
-    uint32_t hi[4], lo[4];
+    uint32_t hi[UNIT / 4], lo[UNIT / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < UNIT / 4; ++i) {
       float p0 = bf16_lo(x[2 * i]) * up, p1 = bf16_hi(x[2 * i]) * up;
       float p2 = bf16_lo(x[2 * i + 1]) * up, p3 = bf16_hi(x[2 * i + 1]) * up;
       const uint32_t h0 = split16(p0, p1), h1 = split16(p2, p3);
       hi[i] = bad ? 0x7F7F7F7Fu : h0 | (h1 << 16);
       lo[i] = bad ? 0x7F7F7F7Fu : cvt2<kE4M3>(p0, p1) | (cvt2<kE4M3>(p2, p3) << 16);
     }
-    uint8_t* base = sq + (ch / 8) * (2 * C::GT * 128) + (((ch & 7) ^ (head & 7)) * 16);
-    *reinterpret_cast<uint4*>(base + head * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(base + (C::GT + head) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    // 128-byte swizzle of the row `head` (8 rows apart the pattern repeats, so row GT + head too)
+    uint8_t* at = sq + (ch >> 7) * (2 * C::GT * 128) + head * 128 + ((((ch >> 4) & 7) ^ (head & 7)) * 16) + (ch & 15);
+    if constexpr (UNIT == 8) {
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + C::GT * 128) = make_uint2(lo[0], lo[1]);
+    } else {
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(at + C::GT * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
     if (ch == 0) cq[head] = a.scale * 1.44269504088896340736f / up;
   }
 };
@@ -366,7 +411,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ps->qfull[i][0]), 4);
       mbar_init(smem_u32(&ps->qfull[i][1]), 4);
-      mbar_init(smem_u32(&ps->sfull[i]), 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(smem_u32(&ps->sfull[i][k]), 1);
+        mbar_init(smem_u32(&ps->sfree[i][k]), 4);
+      }
       mbar_init(smem_u32(&ps->pfull[i]), 4);
       mbar_init(smem_u32(&ps->ofull[i]), 1);
       mbar_init(smem_u32(&ps->drain[i]), 1);
@@ -414,7 +462,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane < nb && tok < w.s.len && tok + a.BR > w.s.st) page = __ldg(trow + pi);
         };
         auto enter = [&]() {               // a segment's first tile
-          h = w.rr / a.HC;
+          h = w.c;
           tok = (w.s.ft + w.t) * kAttnTile + lane * a.BR;
           pi = tok / a.P;
           row = tok - pi * a.P;
@@ -487,9 +535,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int it = 0; it < count; ++it) {
         const int s = it % STAGES;
         const int g = it < 2 * fewer ? it & 1 : longer, j = it < 2 * fewer ? it >> 1 : it - fewer;
-        // the tile; the warpgroup's previous scores, taken before it announces its weights; the queries
+        // the tile; the score buffer, read by the warpgroup two tiles ago; the queries
         if (!attn_wait_warp(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort, limit)) break;
-        if (j > 0 && !attn_wait_warp(smem_u32(&ps->pfull[g]), (j & 1u) ^ 1u, abort, limit)) break;
+        const int par = j & 1;
+        if (j > 1 && !attn_wait_warp(smem_u32(&ps->sfree[g][par]), ((j >> 1) & 1u) ^ 1u, abort, limit)) break;
         const int seg = ps->seg[s];
         if (!attn_wait_warp(smem_u32(&ps->qfull[g][seg & 1]), (seg >> 1) & 1u, abort, limit)) break;
         tc_fence_after();
@@ -499,9 +548,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4 * DCH; ++k)
             if (k < steps)
-              mma_f8(tmem + g * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
+              mma_f8(tmem + (2 * g + par) * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
                      attn_desc(q0 + (k / 4) * (2 * GT * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&ps->sfull[g]));
+          mma_commit(smem_u32(&ps->sfull[g][par]));
         }
         __syncwarp();
       }
@@ -521,7 +570,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (elect_one()) {
           const uint32_t v0 = vlo + uint32_t(s) * (2 * C::KV_BYTES / 16);
           const uint32_t p0 = plo + uint32_t(g) * (C::P_BYTES / 16);
-          const uint32_t o0 = tmem + 2 * C::S_COLS + g * (DCH * C::O_COLS);
+          const uint32_t o0 = tmem + 4 * C::S_COLS + g * (DCH * C::O_COLS);
 #pragma unroll
           for (int c = 0; c < DCH; ++c)
 #pragma unroll
@@ -547,8 +596,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int quad = warp & 3;                   // tensor-memory lanes of this warp
       const int tok = quad * 32 + lane;            // token of the tile; channel of the output
       const uint32_t tlane = uint32_t(quad * 32) << 16;
-      const uint32_t tmem_s = tmem + tlane + wg * C::S_COLS;
-      const uint32_t tmem_o = tmem + tlane + 2 * C::S_COLS + wg * (DCH * C::O_COLS);
+      const uint32_t tmem_s = tmem + tlane + 2 * wg * C::S_COLS;
+      const uint32_t tmem_o = tmem + tlane + 4 * C::S_COLS + wg * (DCH * C::O_COLS);
       const int worker = plan.worker(wg);
       AttnWalk w;
       w.start(a, ps->first_b[wg], ps->first_off[wg], mine);
@@ -568,11 +617,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int seg = 0;; ++seg) {
         bool staging = ahead.next_segment(a);
         if (staging) qn.load(a, ahead, tok);
-        float cq[GT], m[GT], l[GT], o[DCH][GT], fa[GT], fb[GT];
+        // fa, fb: the last tile's factors; lane i of every warp keeps the running maximum of head i % GT
+        float cq[GT], l[GT], o[DCH][GT], fa[GT], fb[GT], m = -INFINITY;
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
           cq[g] = ps->cq[wg][seg & 1][g];
-          m[g] = -INFINITY;
           l[g] = 0.0f;
           fa[g] = fb[g] = 0.0f;
 #pragma unroll
@@ -614,26 +663,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t boxes = ps->boxes[s];
           const bool live = t0 + tok >= w.s.st && t0 + tok < w.s.len && ((boxes >> (tok / a.BR)) & 1u);
           const float sk = live ? sc[tok] : 0.0f, sv = live ? sc[128 + tok] : 0.0f;
-          ok &= attn_wait(smem_u32(&ps->sfull[wg]), par, abort, limit);
+          ok &= attn_wait(smem_u32(&ps->sfull[wg][par]), (j >> 1) & 1u, abort, limit);
           tc_fence_after();
           float x[GT];
           {
             uint32_t r[2 * GT];
-            if constexpr (GT == 8) tmem_ld16(tmem_s, r);
-            else tmem_ld32(tmem_s, r);
+            if constexpr (GT == 8) tmem_ld16(tmem_s + par * C::S_COLS, r);
+            else tmem_ld32(tmem_s + par * C::S_COLS, r);
             tmem_ld_wait();
             tmem_regs_ready(r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ps->sfree[wg][par]));
+            float wm[GT];
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
               const float v = fmaf(__uint_as_float(r[GT + g]), 0.0625f, __uint_as_float(r[g])) * (cq[g] * sk);
               x[g] = live ? v : -INFINITY;
-              const float wm = warp_max(x[g]);
-              if (lane == 0) ps->red[wg][par][quad][g] = wm;
+              wm[g] = warp_max(x[g]);
             }
-          }
-          {
-            const float wm = warp_max(sv);
-            if (lane == 0) ps->redsv[wg][par][quad] = wm;
+            const float wv = warp_max(sv);
+            if (lane == 0) {
+#pragma unroll
+              for (int g = 0; g < GT; g += 4)
+                *reinterpret_cast<float4*>(&ps->red[wg][par][quad][g]) =
+                    make_float4(wm[g], wm[g + 1], wm[g + 2], wm[g + 3]);
+              ps->redsv[wg][par][quad] = wv;
+            }
           }
           if (t > t_first) accumulate(j - 1);
           if (attn_barrier_or(1 + wg, 128, !ok)) {
@@ -645,16 +701,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int E = max(int(__float_as_uint(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))) >> 23) - 126, -110);
           const float rsv = sv * __uint_as_float(uint32_t(8 - E + 127) << 23);
           const float down = __uint_as_float(uint32_t(E - 8 + 127) << 23);
+          // lane i: the factors of head i % GT
+          const int hg = lane & (GT - 1);
+          const float tm = fmaxf(fmaxf(ps->red[wg][par][0][hg], ps->red[wg][par][1][hg]),
+                                 fmaxf(ps->red[wg][par][2][hg], ps->red[wg][par][3][hg]));
+          const float mn = fmaxf(m, tm);
+          const float ref = mn == -INFINITY ? 0.0f : mn;        // nothing valid so far: every factor is 0
+          const float la = ex2(m - ref), lb = ex2(tm - ref), lt = tm == -INFINITY ? 0.0f : tm;
+          m = mn;
 #pragma unroll
           for (int g = 0; g < GT; ++g) {
-            const float tm = fmaxf(fmaxf(ps->red[wg][par][0][g], ps->red[wg][par][1][g]),
-                                   fmaxf(ps->red[wg][par][2][g], ps->red[wg][par][3][g]));
-            const float mn = fmaxf(m[g], tm);
-            const float ref = mn == -INFINITY ? 0.0f : mn;      // nothing valid so far: every factor is 0
-            fa[g] = ex2(m[g] - ref);
-            const float be = ex2(tm - ref);
-            const float p = ex2(x[g] - (tm == -INFINITY ? 0.0f : tm));
-            m[g] = mn;
+            const float p = ex2(x[g] - __shfl_sync(~0u, lt, g));
+            fa[g] = __shfl_sync(~0u, la, g);
+            const float be = __shfl_sync(~0u, lb, g);
             l[g] = fmaf(l[g], fa[g], p * be);
             fb[g] = be * down;
             x[g] = p * rsv;
@@ -674,7 +733,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int i = 0; i < GT / 4; ++i)
             *reinterpret_cast<uint4*>(pr + ((i ^ sw) * 16)) =
                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-          if (!live) {                                          // whatever the cache holds there times 0 is 0
+          if (!live && ((boxes >> (tok / a.BR)) & 1u)) {        // whatever the cache holds there times 0 is 0
             uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(s) * (2 * C::KV_BYTES) + C::KV_BYTES + tok * 128);
 #pragma unroll
             for (int c = 0; c < DCH; ++c)
@@ -693,47 +752,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (failed) break;
         accumulate(j - 1);
         // sums of p over the tokens
-#pragma unroll
-        for (int g = 0; g < GT; ++g) {
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) l[g] += __shfl_xor_sync(~0u, l[g], d);
-          if (lane == 0) ps->lsum[wg][quad][g] = l[g];
+        {
+          const float s1 = warp_sums(l, lane);
+          if ((lane & (32 / GT - 1)) == 0) ps->lsum[wg][quad][lane / (32 / GT)] = s1;
         }
         if (attn_barrier_or(1 + wg, 128, !ok)) break;
-        const int c = w.rr / a.HC, g0 = (w.rr - c * a.HC) * GT;
+        const int g0 = w.hc * GT, heads = min(GT, a.G - g0);
         const bool whole = t_first == 0 && w.t1 == w.s.n;
-        const int heads = min(GT, a.G - g0);
-        const int64_t head0 = int64_t(w.b) * (int64_t(a.H) * a.G) + int64_t(c) * a.G + g0;
+        const int64_t head0 = (int64_t(w.b) * a.H + w.c) * a.G + g0;
         const int slot = 2 * worker + (seg > 0 ? 1 : 0);
-        // lane g: the sum of head g, for the warp
-        const int hg = lane < GT ? lane : 0;
+        // lane i: the sum of head i % GT
+        const int hg = lane & (GT - 1);
         const float sum = (ps->lsum[wg][0][hg] + ps->lsum[wg][1][hg]) + (ps->lsum[wg][2][hg] + ps->lsum[wg][3][hg]);
-        const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;     // no valid token: zeros
-#pragma unroll
-        for (int g = 0; g < GT; ++g) {
-          if (g < heads && tok == g) {
-            if (!whole) {
-              a.ws_ml[(int64_t(slot) * 2) * GT + g] = m[g];
-              a.ws_ml[(int64_t(slot) * 2 + 1) * GT + g] = sum;
-            } else if (a.lse != nullptr) {
-              a.lse[head0 + g] = sum == 0.0f ? -INFINITY : (m[g] + __log2f(sum)) * 0.69314718055994530942f;
-            }
+        if (tok < heads) {
+          if (!whole) {
+            a.ws_ml[int64_t(slot) * 2 * GT + tok] = m;
+            a.ws_ml[int64_t(slot) * 2 * GT + GT + tok] = sum;
+          } else if (a.lse != nullptr) {
+            a.lse[head0 + tok] = sum == 0.0f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994530942f;
           }
-          const float f = __shfl_sync(~0u, inv, g);
-#pragma unroll
-          for (int ch = 0; ch < DCH; ++ch) o[ch][g] *= f;
         }
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);        // no valid token: zeros
 #pragma unroll
         for (int ch = 0; ch < DCH; ++ch) {
-          if (ch * 128 + tok < a.D) {
+          const bool on = ch * 128 + tok < a.D;
+          if (whole) {
             __nv_bfloat16* po = reinterpret_cast<__nv_bfloat16*>(a.out) + head0 * a.D + ch * 128 + tok;
+#pragma unroll
+            for (int g = 0; g < GT; ++g) {
+              const float v = o[ch][g] * __shfl_sync(~0u, inv, g);
+              if (on && g < heads) *po = __float2bfloat16_rn(v);
+              po += a.D;
+            }
+          } else {
             float* pw = a.ws_o + int64_t(slot) * GT * a.D + ch * 128 + tok;
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-              if (g < heads) {
-                if (whole) po[g * a.D] = __float2bfloat16_rn(o[ch][g]);
-                else pw[g * a.D] = o[ch][g];
-              }
+              if (on && g < heads) *pw = o[ch][g];
+              pw += a.D;
             }
           }
         }
@@ -743,7 +799,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int64_t last = int64_t(plan.begin(worker)) + j - w.t1 + w.s.n - 1;
             info = make_int2(slot, int(((last + 1) * plan.workers + plan.total - 1) / plan.total) - 1);
           }
-          a.ws_row[int64_t(w.b) * (a.H * a.HC) + w.rr] = info;
+          a.ws_row[(int64_t(w.b) * a.H + w.c) * a.HC + w.hc] = info;
         }
         if (!w.next_segment(a)) break;
       }
@@ -756,50 +812,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Rows that more than one worker has a part of: their partial sums added up in the order of the
-// tiles.  One block per row and head; its warps take the partials in turn.
+// tiles.  One block per row and head: first every partial's factor (its maximum against the
+// largest), then the sums, the warps taking the partials in turn, 16 bytes a lane and several
+// loads in flight.  Bound by the latency of these two dependent rounds of loads.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinMax = 1024;      // partials of one row: at most two workers an SM
+
 template <int GT>
-__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a) {
-  pdl_wait();
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnArgs a) {
+  constexpr int W = kJoinThreads / 32;
+  __shared__ float sf[kJoinMax];
+  __shared__ float sm[W], sl[W];
+  __shared__ __align__(16) float so[W][256];
   pdl_trigger();
-  __shared__ float so[4][256];
-  __shared__ float sl[4];
+  pdl_wait();
   const int64_t row = blockIdx.x;
   const int2 info = a.ws_row[row];
   if (info.x < 0) return;
-  const int g = blockIdx.y, rr = int(row % (a.H * a.HC));
-  const int c = rr / a.HC, g0 = (rr % a.HC) * GT;
-  if (g0 + g >= a.G) return;
+  const int g = blockIdx.y, hc = int(row % a.HC);
+  if (hc * GT + g >= a.G) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = info.y - info.x / 2 + 1;
-  auto slot_of = [&](int i) { return i == 0 ? info.x : 2 * (info.x / 2 + i); };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.ws_ml[int64_t(slot_of(i)) * 2 * GT + g]);
-  m = warp_max(m);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float o[8], l = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-  for (int i = warp; i < n; i += 4) {
-    const int64_t s = slot_of(i);
-    const float f = ex2(a.ws_ml[s * 2 * GT + g] - ref);
-    l = fmaf(f, a.ws_ml[(s * 2 + 1) * GT + g], l);
-    const float* p = a.ws_o + (s * GT + g) * a.D;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j * 32 + lane < a.D) o[j] = fmaf(f, p[j * 32 + lane], o[j]);
+  const int n = min(info.y - info.x / 2 + 1, kJoinMax);
+  auto slot_of = [&](int i) { return int64_t(i == 0 ? info.x : 2 * (info.x / 2 + i)); };
+  float m = -INFINITY, l = 0.0f;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+    const float* p = a.ws_ml + slot_of(i) * 2 * GT + g;
+    const float mi = p[0], li = p[GT];
+    sf[i] = mi;
+    const float mn = fmaxf(m, mi);
+    l = l * ex2(m == mn ? 0.0f : m - mn) + li * ex2(mi == mn ? 0.0f : mi - mn);
+    m = mn;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) so[warp][j * 32 + lane] = o[j];
-  if (lane == 0) sl[warp] = l;
+  const float wm = warp_max(m);
+  if (lane == 0) sm[warp] = wm;
   __syncthreads();
-  l = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-  const int64_t head = (row / (a.H * a.HC)) * (int64_t(a.H) * a.G) + int64_t(c) * a.G + g0 + g;
-  for (int d = threadIdx.x; d < a.D; d += 128) {
-    const float v = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
+  float top = sm[0];
+#pragma unroll
+  for (int i = 1; i < W; ++i) top = fmaxf(top, sm[i]);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  l *= ex2(m - ref);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+  if (lane == 0) sl[warp] = l;
+  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  const bool on0 = lane * 4 < a.D, on1 = lane * 4 + 128 < a.D;
+#pragma unroll 4
+  for (int i = warp; i < n; i += W) {
+    const float* p = a.ws_o + (slot_of(i) * GT + g) * a.D + lane * 4;
+    const float f = ex2(sf[i] - ref);
+    const float4 x = on0 ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 y = on1 ? *reinterpret_cast<const float4*>(p + 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+    o[0] = make_float4(fmaf(f, x.x, o[0].x), fmaf(f, x.y, o[0].y), fmaf(f, x.z, o[0].z), fmaf(f, x.w, o[0].w));
+    o[1] = make_float4(fmaf(f, y.x, o[1].x), fmaf(f, y.y, o[1].y), fmaf(f, y.z, o[1].z), fmaf(f, y.w, o[1].w));
+  }
+  reinterpret_cast<float4*>(so[warp])[lane] = o[0];
+  reinterpret_cast<float4*>(so[warp])[32 + lane] = o[1];
+  __syncthreads();
+  l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) l += sl[i];
+  const int64_t head = row / a.HC * a.G + hc * GT + g;
+  const int d = threadIdx.x;
+  if (d < a.D) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += so[i][d];
     reinterpret_cast<__nv_bfloat16*>(a.out)[head * a.D + d] = __float2bfloat16_rn(l == 0.0f ? 0.0f : v / l);
   }
   if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[head] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+    a.lse[head] = l == 0.0f ? -INFINITY : (top + __log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace fp8lin

@@ -52,9 +52,9 @@ struct KvWriteArgs {
   const int64_t* pos;       // [T]
   const int64_t* slots;     // [T]
   KvCache c;
-  int64_t T, max_pos;
-  float eps;
-  int Hq, Hk, Hv, D, R;     // heads of q, k and v that this call handles
+  int64_t max_pos;
+  float eps, inv_d;         // inv_d = 1 / D
+  int T, Hq, Hk, Hv, D, R;     // heads of q, k and v that this call handles
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -62,147 +62,194 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// LPH lanes own one head of one token, 8 channels each as two runs of 4 (a, b): adjacent
-// runs, or, for pairs (i, R/2 + i), the two runs that rotate into each other, so that the
-// rotation never leaves a thread.  A group of lanes takes U consecutive heads of a token:
-// their loads are in flight together and share the token's cosines and sines.
-template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
+// LPH lanes own one head of one token, 16 channels each as two runs of 8 (a, b): for pairs
+// (i, R/2 + i) the two runs that rotate into each other, so that the rotation never leaves a
+// thread, else run j of each half of the head.  Loads and bf16 stores are 16 bytes a lane and
+// adjacent over the lanes.  A group of lanes keeps its head and goes from token to token:
+// pointers and the norm's weights are set up once, no index is divided in the loop, and the
+// channels of the next kWriteAhead tokens are on their way through shared memory meanwhile.
+// Issue slots bound it next to memory (about 200 instructions a lane and head against 64 bytes
+// moved), hence packed fp32 pairs throughout.  16384 tokens of 32 + 8 + 8 heads of 128 in one
+// pass: XX us, XX TB/s; with 8 channels a lane, scalar arithmetic and no look-ahead 133 us.
+constexpr int kWriteAhead = 3;
+
+template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
 __global__ void __launch_bounds__(256) k_norm_rope_write(const KvWriteArgs a) {
   pdl_wait();
   pdl_trigger();
   const int heads = a.Hq + a.Hk + a.Hv;
-  const int hb = (heads + U - 1) / U;
   const int j = threadIdx.x & (LPH - 1);
-  const int64_t total = a.T * hb;
-  const int64_t stride = int64_t(gridDim.x) * (256 / LPH);
-  const bool lane_on = j * 8 < a.D;
-  int ca = 8 * j, cb = 8 * j + 4;
-  const bool turned = ROPE != kRopeNone && 8 * j < a.R;
-  if (ROPE == kRopeHalves && turned) {
-    ca = 4 * j;
-    cb = a.R / 2 + 4 * j;
+  const int group = (int(blockIdx.x) * 256 + int(threadIdx.x)) / LPH;
+  const int step = int(gridDim.x) * (256 / LPH) / heads;   // tokens at a time; at least one (host)
+  const int t0 = group / heads;
+  const int h = group - t0 * heads;
+  const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
+  const int hc = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hk;
+  const bool on = t0 < step && j * 16 < a.D;
+  // the runs, and whether and by which pairs they turn
+  int ca = 8 * j, cb = a.D / 2 + 8 * j, pa = 0, pb = 0;
+  bool ta = false, tb = false;
+  if (ROPE == kRopeHalves) {
+    ta = tb = 16 * j < a.R;
+    pa = 8 * j;
+    pb = 8 * j + 4;
+    ca = ta ? 8 * j : 16 * j;
+    cb = ta ? a.R / 2 + 8 * j : 16 * j + 8;
+  } else if (ROPE == kRopeInterleaved) {
+    ta = ca < a.R;
+    tb = cb < a.R;
+    pa = ca / 2;
+    pb = cb / 2;
   }
+  if (ROPE != kRopeNone && !(on && (is_q || is_k))) ta = tb = false;
+  const uint16_t* src = is_q ? a.q + hc * a.q_head : is_k ? a.k + hc * a.k_head : a.v + hc * a.v_head;
+  const int64_t src_tok = is_q ? a.q_tok : is_k ? a.k_tok : a.v_tok;
+  const uint16_t* wn = is_q ? a.wq : is_k ? a.wk : nullptr;
+  const bool norm_warp = __any_sync(0xffffffffu, wn != nullptr);
+  const bool to_cache = CACHE && !is_q, cache_warp = __any_sync(0xffffffffu, to_cache);
+  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+  if (wn != nullptr && on) {
+    wa = __ldg(reinterpret_cast<const uint4*>(wn + ca));
+    wb = __ldg(reinterpret_cast<const uint4*>(wn + cb));
+  }
+  // tokens ahead, in shared memory: every thread reads only what it copied itself
+  __shared__ uint4 ring[kWriteAhead + 1][2][256];
+  if (!on)
+    for (int i = 0; i <= kWriteAhead; ++i) ring[i][0][threadIdx.x] = ring[i][1][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](int t, int s) {
+    if (on && t < a.T) {
+      const uint16_t* p = src + t * src_tok;
+      cp_async16(smem_u32(&ring[s][0][threadIdx.x]), p + ca);
+      cp_async16(smem_u32(&ring[s][1][threadIdx.x]), p + cb);
+    }
+    cp_async_commit();
+  };
+  int64_t pos = 0, slot = -1;
+  auto fetch_index = [&](int t) {
+    if (on && t < a.T) {
+      if (ROPE != kRopeNone && (ta || tb)) pos = __ldg(a.pos + t);
+      if (CACHE && to_cache) slot = __ldg(a.slots + t);
+    }
+  };
+  fetch_index(t0);
+#pragma unroll
+  for (int i = 0; i < kWriteAhead; ++i) fetch(t0 + i * step, i);
+  int s = 0;
   // every lane of a warp walks the same number of steps (the shuffles below need them all)
-  for (int64_t i0 = int64_t(blockIdx.x) * (256 / LPH); i0 < total; i0 += stride) {
-    const int64_t item = i0 + threadIdx.x / LPH;
-    const bool item_on = item < total;
-    const int64_t t = item_on ? item / hb : 0;
-    const int h0 = item_on ? int(item - t * hb) * U : heads;
-    int64_t slot = -1;
-    if (CACHE && item_on) slot = __ldg(a.slots + t);
-    uint2 x[U][2];
+  for (int tb0 = 0; tb0 < a.T; tb0 += step) {
+    const int t = tb0 + t0;
+    const bool live = on && t < a.T;
+    fetch(t + kWriteAhead * step, s == 0 ? kWriteAhead : s - 1);
+    cp_async_wait<kWriteAhead>();
+    const uint4 xa = ring[s][0][threadIdx.x], xb = ring[s][1][threadIdx.x];
+    s = s == kWriteAhead ? 0 : s + 1;
+    const uint32_t w8[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+    const int64_t p = min(max(pos, int64_t(0)), a.max_pos - 1), sl = slot;
+    fetch_index(t + step);
+    uint64_t y[8];                                         // pairs of channels: run a, run b
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u;
-      x[u][0] = x[u][1] = make_uint2(0u, 0u);
-      if (h < heads && lane_on) {
-        const uint16_t* p = h < a.Hq ? a.q + t * a.q_tok + h * a.q_head
-                            : h < a.Hq + a.Hk ? a.k + t * a.k_tok + (h - a.Hq) * a.k_head
-                                              : a.v + t * a.v_tok + (h - a.Hq - a.Hk) * a.v_head;
-        if (ROPE == kRopeHalves) {
-          x[u][0] = *reinterpret_cast<const uint2*>(p + ca);
-          x[u][1] = *reinterpret_cast<const uint2*>(p + cb);
-        } else {
-          const uint4 y = *reinterpret_cast<const uint4*>(p + ca);
-          x[u][0] = make_uint2(y.x, y.y);
-          x[u][1] = make_uint2(y.z, y.w);
-        }
+    for (int i = 0; i < 8; ++i) y[i] = pack2(bf16_lo(w8[i]), bf16_hi(w8[i]));
+    // HALVES: the eight pairs' cosines and sines; INTERLEAVED: four of run a, four of run b
+    float4 cs[2], sn[2];
+    if (ROPE != kRopeNone) {
+      cs[0] = cs[1] = sn[0] = sn[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* row = a.cos_sin + p * a.R;
+      if (ta && live) {
+        cs[0] = __ldg(reinterpret_cast<const float4*>(row + pa));
+        sn[0] = __ldg(reinterpret_cast<const float4*>(row + a.R / 2 + pa));
+      }
+      if (tb && live) {
+        cs[1] = __ldg(reinterpret_cast<const float4*>(row + pb));
+        sn[1] = __ldg(reinterpret_cast<const float4*>(row + a.R / 2 + pb));
       }
     }
-    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ROPE != kRopeNone && turned && item_on && h0 < a.Hq + a.Hk) {
-      const int64_t p = min(max(__ldg(a.pos + t), int64_t(0)), a.max_pos - 1);
-      const float* row = a.cos_sin + p * a.R + 4 * j;
-      cs = __ldg(reinterpret_cast<const float4*>(row));
-      sn = __ldg(reinterpret_cast<const float4*>(row + a.R / 2));
-    }
+    if (norm_warp) {                                       // its sum needs every lane of the group
+      uint64_t s0 = mul2(y[0], y[0]), s1 = mul2(y[4], y[4]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u;
-      const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk, is_v = !is_q && !is_k && h < heads;
-      const uint32_t w4[4] = {x[u][0].x, x[u][0].y, x[u][1].x, x[u][1].y};
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[2 * i] = bf16_lo(w4[i]);
-        y[2 * i + 1] = bf16_hi(w4[i]);
+      for (int i = 1; i < 4; ++i) {
+        s0 = fma2(y[i], y[i], s0);
+        s1 = fma2(y[4 + i], y[4 + i], s1);
       }
-      const uint16_t* wn = is_q ? a.wq : is_k ? a.wk : nullptr;
-      // the norm's sum needs every lane of the group, so the whole warp takes part
-      if (__any_sync(0xffffffffu, wn != nullptr)) {
-        float ss = 0.0f;
+      const float2 u = unpack2(s0), v = unpack2(s1);
+      float ss = (u.x + u.y) + (v.x + v.y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+      for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      if (wn != nullptr) {
+        const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+        const uint32_t g8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-        for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        if (wn != nullptr && lane_on) {
-          const float r = 1.0f / sqrtf(ss / float(a.D) + a.eps);
-          const uint2 wa = __ldg(reinterpret_cast<const uint2*>(wn + ca));
-          const uint2 wb = __ldg(reinterpret_cast<const uint2*>(wn + cb));
-          const uint32_t v4[4] = {wa.x, wa.y, wb.x, wb.y};
+        for (int i = 0; i < 8; ++i)
+          y[i] = mul2(mul2(y[i], pack2(r, r)), pack2(bf16_lo(g8[i]), bf16_hi(g8[i])));
+      }
+    }
+    if (ROPE != kRopeNone) {
+      const float c8[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
+      const float s8[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
+      if (ROPE == kRopeHalves) {
+        if (ta) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            y[2 * i] = y[2 * i] * r * bf16_lo(v4[i]);
-            y[2 * i + 1] = y[2 * i + 1] * r * bf16_hi(v4[i]);
+            const uint64_t c = pack2(c8[2 * i], c8[2 * i + 1]), s = pack2(s8[2 * i], s8[2 * i + 1]);
+            const uint64_t n = pack2(-s8[2 * i], -s8[2 * i + 1]), m0 = y[i], m1 = y[4 + i];
+            y[i] = fma2(m1, n, mul2(m0, c));
+            y[4 + i] = fma2(m0, s, mul2(m1, c));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i < 4 ? ta : tb) {
+            const float2 m = unpack2(y[i]);
+            y[i] = fma2(pack2(m.y, m.x), pack2(-s8[i], s8[i]), mul2(y[i], pack2(c8[i], c8[i])));
           }
         }
       }
-      if (ROPE != kRopeNone && turned && (is_q || is_k)) {
-        const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+    }
+    if (CACHE && cache_warp) {
+      float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ia = ROPE == kRopeInterleaved ? 2 * i : i, ib = ROPE == kRopeInterleaved ? 2 * i + 1 : 4 + i;
-          const float n0 = y[ia], n1 = y[ib];
-          y[ia] = n0 * c[i] - n1 * s[i];
-          y[ib] = n1 * c[i] + n0 * s[i];
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2(y[i]);
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
       }
-      if (CACHE) {
-        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+      for (int d = LPH / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (to_cache && live && sl >= 0 && sl < a.c.pages * a.c.P) {     // under 2^31 (host)
+        const GroupScale<FMT, SF> sc(m);
+        const int page = int(sl) / a.c.P, row = int(sl) - page * a.c.P;
+        uint8_t* out = (is_k ? a.c.k : a.c.v) + page * a.c.page_stride + hc * a.c.head_stride + row * a.c.token_stride;
+        uint32_t c[8];
 #pragma unroll
-        for (int d = LPH / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if ((is_k || is_v) && slot >= 0 && slot < a.c.pages * a.c.P) {
-          const GroupScale<FMT, SF> sc(m);
-          uint32_t c[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = cvt2<FMT>(sc.apply(y[2 * i]), sc.apply(y[2 * i + 1]));
-          const uint2 code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-          const int64_t page = slot / a.c.P, row = slot - page * a.c.P;
-          const int hc = is_k ? h - a.Hq : h - a.Hq - a.Hk;
-          uint8_t* dst = (is_k ? a.c.k : a.c.v) + page * a.c.page_stride + hc * a.c.head_stride + row * a.c.token_stride;
-          if (lane_on) {
-            if (ROPE == kRopeHalves) {
-              *reinterpret_cast<uint32_t*>(dst + ca) = code.x;
-              *reinterpret_cast<uint32_t*>(dst + cb) = code.y;
-            } else {
-              *reinterpret_cast<uint2*>(dst + ca) = code;
-            }
-          }
-          if (j == 0) (is_k ? a.c.ks : a.c.vs)[(page * a.c.H + hc) * a.c.P + row] = sc.s;
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = unpack2(sc.apply2(y[i]));
+          c[i] = cvt2<FMT>(v.x, v.y);
         }
+        *reinterpret_cast<uint2*>(out + ca) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        *reinterpret_cast<uint2*>(out + cb) = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
+        if (j == 0) (is_k ? a.c.ks : a.c.vs)[(int64_t(page) * a.c.H + hc) * a.c.P + row] = sc.s;
       }
-      if ((is_q || (!CACHE && is_k)) && lane_on) {
-        uint16_t* p = is_q ? a.qo + t * a.qo_tok + h * a.qo_head : a.ko + t * a.ko_tok + (h - a.Hq) * a.ko_head;
-        const uint2 oa = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
-        const uint2 ob = make_uint2(bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
-        if (ROPE == kRopeHalves) {
-          *reinterpret_cast<uint2*>(p + ca) = oa;
-          *reinterpret_cast<uint2*>(p + cb) = ob;
-        } else {
-          *reinterpret_cast<uint4*>(p + ca) = make_uint4(oa.x, oa.y, ob.x, ob.y);
-        }
+    }
+    if (live && !to_cache) {
+      uint16_t* out = is_q ? a.qo + t * a.qo_tok + hc * a.qo_head : a.ko + t * a.ko_tok + hc * a.ko_head;
+      uint32_t r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2(y[i]);
+        r[i] = bf16x2(v.x, v.y);
       }
+      *reinterpret_cast<uint4*>(out + ca) = make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4*>(out + cb) = make_uint4(r[4], r[5], r[6], r[7]);
     }
   }
 }
 
 // ------------------------------------------------------------------- read back
-// Row r of the outputs is token r - offsets[b] of the sequence b whose range holds r.  One
-// warp per row: a binary search of the offsets, then 16 channels per lane and step of its
-// k and v heads.  Rows whose page is not in the cache are zeros; rows outside every range
-// are not written.
+// Row r of the outputs is token r - offsets[b] of the sequence b whose range holds r.  A warp
+// takes a run of rows, so that it searches the offsets once and reads the table once a page;
+// its steps are slices of 128 16-channel chunks of a row (k's heads, then v's), four chunks a
+// lane, and the next step's codes are loaded before this one's are converted.  Rows whose page
+// is not in the cache are zeros; rows outside every range are not written.
+// Bound by memory, two thirds of it the bf16 stores: XX
 struct KvReadArgs {
   KvCache c;
   const int32_t* table;     // [B][max_pages]
@@ -211,6 +258,8 @@ struct KvReadArgs {
   uint16_t* vo;
   int64_t table_stride, max_pages, rows;
   int B;
+  uint32_t cph_magic;       // ceil(2^32 / (D / 16)): quotients by multiplication; 0 for D = 16
+  int run;                  // rows per warp
 };
 
 // 4 codes -> 4 fp32 values times s, as two bf16 pairs.
@@ -229,57 +278,100 @@ __device__ __forceinline__ uint2 dec4(uint32_t w, float s) {
   return make_uint2(bf16x2(f0.x * s, f0.y * s), bf16x2(f1.x * s, f1.y * s));
 }
 
+// 32 bytes in one store (two 16-byte stores would each write half of every sector).
+__device__ __forceinline__ void store32(void* p, uint2 a, uint2 b, uint2 c, uint2 d) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(b.x),
+               "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
+               : "memory");
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(256) k_kv_read(const KvReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int cph = a.c.D / 16;                 // 16-channel chunks per head
+  const int cph = a.c.D / 16;                 // chunks per head
   const int chunks = a.c.H * cph;             // of k, and as many of v
-  const int64_t nwarp = int64_t(gridDim.x) * 8;
-  for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows; r += nwarp) {
-    if (r < __ldg(a.offsets) || r >= __ldg(a.offsets + a.B)) continue;
-    int lo = 0, hi = a.B;                     // offsets[lo] <= r < offsets[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.offsets + mid) <= r) lo = mid;
-      else hi = mid;
-    }
-    const int64_t tok = r - __ldg(a.offsets + lo);
-    const int64_t pi = tok / a.c.P, row = tok - pi * a.c.P;
-    int64_t page = tok >= 0 && pi < a.max_pages ? __ldg(a.table + lo * a.table_stride + pi) : -1;
-    const bool ok = page >= 0 && page < a.c.pages;
+  const int64_t warp = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  int64_t r = max(warp * a.run, int64_t(__ldg(a.offsets)));
+  const int64_t end = min(min((warp + 1) * a.run, a.rows), int64_t(__ldg(a.offsets + a.B)));
+  if (r >= end) return;
+  int b = 0;                                  // offsets[b] <= r < offsets[b + 1]
+  for (int hi = a.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (__ldg(a.offsets + mid) <= r) b = mid;
+    else hi = mid;
+  }
+  int64_t next_b = __ldg(a.offsets + b + 1);
+  int tok = int(r - __ldg(a.offsets + b));
+  int pi = tok / a.c.P, row = tok - pi * a.c.P;
+  int64_t page;
+  auto turn = [&]() {                         // the page of the current token
+    page = pi < a.max_pages ? __ldg(a.table + b * a.table_stride + pi) : -1;
+    if (page >= a.c.pages) page = -1;
+  };
+  turn();
+  int first = 0;                              // the step's first chunk
+  uint4 q[4];
+  float s[4];
+  auto load = [&]() {
     const int64_t src = page * a.c.page_stride + row * a.c.token_stride;
-    for (int i0 = 0; i0 < 2 * chunks; i0 += 128) {
-      uint4 q[4];
-      float s[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * 32 + lane;
-        q[u] = make_uint4(0u, 0u, 0u, 0u);
-        s[u] = 0.0f;
-        if (ok && i < 2 * chunks) {
-          const bool is_v = i >= chunks;
-          const int c = is_v ? i - chunks : i;
-          const int h = c / cph;
-          q[u] = ldg_stream(reinterpret_cast<const uint4*>((is_v ? a.c.v : a.c.k) + src + h * a.c.head_stride +
-                                                           (c - h * cph) * 16));
-          s[u] = __ldg((is_v ? a.c.vs : a.c.ks) + (page * a.c.H + h) * a.c.P + row);
-        }
+    for (int u = 0; u < 4; ++u) {
+      const int i = first + u * 32 + lane;
+      q[u] = make_uint4(0u, 0u, 0u, 0u);
+      s[u] = 0.0f;
+      if (page >= 0 && i < 2 * chunks) {
+        const bool is_v = i >= chunks;
+        const int c = is_v ? i - chunks : i;
+        const int h = a.cph_magic != 0u ? int(__umulhi(uint32_t(c), a.cph_magic)) : c;
+        q[u] = ldg_stream(reinterpret_cast<const uint4*>((is_v ? a.c.v : a.c.k) + src + h * a.c.head_stride +
+                                                         (c - h * cph) * 16));
+        s[u] = __ldg((is_v ? a.c.vs : a.c.ks) + (page * a.c.H + h) * a.c.P + row);
       }
+    }
+  };
+  load();
+  while (true) {
+    uint4 v[4];
+    float f[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * 32 + lane;
-        if (i < 2 * chunks) {
-          const bool is_v = i >= chunks;
-          uint4* dst = reinterpret_cast<uint4*>((is_v ? a.vo : a.ko) + (r * chunks + (is_v ? i - chunks : i)) * 16);
-          const uint2 y0 = dec4<FMT>(q[u].x, s[u]), y1 = dec4<FMT>(q[u].y, s[u]);
-          const uint2 y2 = dec4<FMT>(q[u].z, s[u]), y3 = dec4<FMT>(q[u].w, s[u]);
-          dst[0] = make_uint4(y0.x, y0.y, y1.x, y1.y);
-          dst[1] = make_uint4(y2.x, y2.y, y3.x, y3.y);
+    for (int u = 0; u < 4; ++u) {
+      v[u] = q[u];
+      f[u] = s[u];
+    }
+    const int64_t at = r;
+    const int from = first;
+    first += 128;
+    if (first >= 2 * chunks) {                // the next row
+      first = 0;
+      if (++r < end) {
+        if (r >= next_b) {                    // the next sequence that has a row
+          do next_b = __ldg(a.offsets + ++b + 1);
+          while (r >= next_b);
+          pi = row = 0;
+          turn();
+        } else if (++row == a.c.P) {
+          row = 0;
+          ++pi;
+          turn();
         }
       }
     }
+    const bool more = r < end;
+    if (more) load();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = from + u * 32 + lane;
+      if (i < 2 * chunks) {
+        const bool is_v = i >= chunks;
+        uint16_t* dst = (is_v ? a.vo : a.ko) + (at * chunks + (is_v ? i - chunks : i)) * 16;
+        const uint2 y0 = dec4<FMT>(v[u].x, f[u]), y1 = dec4<FMT>(v[u].y, f[u]);
+        const uint2 y2 = dec4<FMT>(v[u].z, f[u]), y3 = dec4<FMT>(v[u].w, f[u]);
+        store32(dst, y0, y1, y2, y3);
+      }
+    }
+    if (!more) break;
   }
 }
 

@@ -100,6 +100,16 @@ struct GroupScale {
     }
     return __fmul_rn(x, rinv);
   }
+  // The same for two values in packed instructions.
+  __device__ __forceinline__ uint64_t apply2(uint64_t x) const {
+    if (SF != kScaleFp32) return mul2(x, pack2(rinv, rinv));
+    const uint64_t r2 = pack2(rinv, rinv);
+    const uint64_t xs = mul2(x, pack2(pre, pre));
+    const uint64_t q0 = mul2(xs, r2);
+    const uint64_t e = fma2(q0, pack2(-ss, -ss), xs);
+    const float2 q = unpack2(fma2(e, r2, q0)), xv = unpack2(x);
+    return pack2(copysignf(q.x, xv.x), copysignf(q.y, xv.y));
+  }
 };
 
 // Two fp32 -> two FP8 codes in one 16-bit word; `lo` lands in the low byte.

@@ -346,7 +346,8 @@ int fp8_moe_gemm(const void* qa, const float* sa, const void* qw, const float* s
  *               bytes, multiples of 16, >= head_dim, < 2^40; k, v 16-byte aligned.
  *               Different (page, h, row) must not overlap.
  *   k_scale, v_scale   DEVICE fp32 [num_pages][heads][page_size], 16-byte aligned.
- *   head_dim    D % 16 == 0, D <= 256.  page_size % 8 == 0.  num_pages < 2^31 - 1.
+ *   head_dim    D % 16 == 0, D <= 256.  page_size % 8 == 0.
+ *               num_pages * page_size < 2^31.
  *   fmt, scale_fmt   fp8_format, fp8_scale_fmt (scale_fmt matters to the writers only).
  * No initial contents are required: readers use nothing beyond the lengths they are given.
  */
@@ -409,7 +410,7 @@ int fp8_qk_norm_rope_kv_write(const void* q, int64_t q_tok, int64_t q_head, cons
  *   table      DEVICE int32 [B][max_pages], row stride table_stride >= max_pages: page ids.
  *   offsets    DEVICE int32 [B + 1], non-decreasing: rows [offsets[b], offsets[b + 1]) of the
  *              outputs are tokens 0, 1, ... of sequence b.
- *   ko, vo     bf16 [rows][heads][D], 16-byte aligned.  Rows outside every range are not
+ *   ko, vo     bf16 [rows][heads][D], 32-byte aligned.  Rows outside every range are not
  *              written; tokens beyond the table or of a page outside the cache are zeros.
  */
 int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_stride, int64_t max_pages,
