@@ -105,7 +105,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.fmt, self.scale_fmt = fmt, scale_fmt
         self.num_pages, self.heads, self.page_size, self.head_dim = pages, heads, page, dim
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page,
                                     heads, dim, k.stride(0), k.stride(1), k.stride(2), fmt, scale_fmt)
         self._ref = ctypes.addressof(self._struct)
@@ -120,29 +120,38 @@ def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, device="cud
 
 
 # ------------------------------------------------------------ argument checks
-_NO_GUARD = contextlib.nullcontext()
+# A decode step makes these calls once a layer, so the checks touch every property of a tensor
+# once and the current device and stream are read without building torch objects.
+_BF16, _F32, _I64, _I32 = torch.bfloat16, torch.float32, torch.int64, torch.int32
 
 
-def _on(device: torch.device, *tensors):
-    """Checks that the tensors live on `device`, a CUDA device; the guard that makes it current."""
-    if device.type != "cuda":
+def _check_devices(index: int, *tensors) -> None:
+    """The tensors live on the CUDA device of that index (-1: not a CUDA device)."""
+    if index < 0:
         raise ValueError("fp8 library tensors must live on a CUDA device")
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor lives on {t.device}, the others on {device}")
-    return _NO_GUARD if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor lives on {t.device}, the others on cuda:{index}")
 
 
-def _stream_of(stream) -> int:
+def _call(name: str, fn, index: int, stream, args) -> None:
+    """fn(*args, stream) with the device `index` current; the current stream unless one is given."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(name, fn, index, stream, args)
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    code = fn(*args, stream)
+    if code:
+        _check(name, code)
 
 
 def _alloc(device: torch.device, stream):
     """The context in which a short name allocates: the stream that will write the memory."""
     if stream is None:
-        return _NO_GUARD
+        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
@@ -150,18 +159,18 @@ def _alloc(device: torch.device, stream):
 
 def _rows(t: torch.Tensor, name: str, shape: tuple) -> tuple:
     """(pointer, token stride, head stride) of a bf16 [tokens, heads, D] view."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name} needs contiguous channels, got strides {s}")
-    return t.data_ptr(), s[0], s[1]
+    tok, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} needs contiguous channels, got strides {t.stride()}")
+    return t.data_ptr(), tok, head
 
 
 def _vec(t: torch.Tensor, name: str, n: int, dtype) -> int:
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected a contiguous ({n},)")
@@ -172,26 +181,31 @@ def _rope(positions, cos_sin, T: int) -> tuple:
     """(cos_sin pointer, max_pos, R, pos pointer); no rotation without a table."""
     if cos_sin is None:
         return None, 0, 0, None
-    if cos_sin.dtype != torch.float32:
+    if cos_sin.dtype is not _F32:
         raise TypeError(f"cos_sin has dtype {cos_sin.dtype}, expected torch.float32")
     if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError(f"cos_sin must be a contiguous [max_pos, R], got {tuple(cos_sin.shape)}")
     if positions is None:
         raise ValueError("a rotation needs positions")
-    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], _vec(positions, "positions", T, torch.int64)
+    return cos_sin.data_ptr(), *cos_sin.shape, _vec(positions, "positions", T, _I64)
 
 
 def _weight(w, name: str, D: int):
-    return None if w is None else _vec(w, name, D, torch.bfloat16)
+    return None if w is None else _vec(w, name, D, _BF16)
 
 
 def _table(table: torch.Tensor, B: int) -> tuple:
-    if table.dtype != torch.int32:
+    """(pointer, row stride, pages per row)."""
+    if table.dtype is not _I32:
         raise TypeError(f"table has dtype {table.dtype}, expected torch.int32")
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dim() != 2:
+        raise ValueError(f"table must be [{B}, max_pages], got {tuple(table.shape)}")
+    rows, pages = table.shape
+    row, one = table.stride()
+    if rows != B or (pages > 1 and one != 1):
         raise ValueError(f"table must be [{B}, max_pages] with contiguous rows, got {tuple(table.shape)}")
     # the row stride of one row, or of an empty one, may be anything: no second row is read
-    return table.data_ptr(), max(table.stride(0), table.shape[1]) if B <= 1 else table.stride(0), table.shape[1]
+    return table.data_ptr(), max(row, pages) if B <= 1 else row, pages
 
 
 # ---------------------------------------------------------------- C names
@@ -200,19 +214,15 @@ def fp8_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, wq=None, wk=None, e
     """RMS norm per head (weights wq, wk bf16 [D]; None: no norm) and rotation of bf16 q [T, Hq, D]
     and k [T, Hk, D] (views with any token and head strides) into q_out, k_out, which may be q
     and k.  cos_sin: rope_table's fp32 [max_pos, R], or None."""
-    T, Hq, D = q.shape
+    T, Hq, D = shape = q.shape
     Hk = k.shape[1]
-    guard = _on(q.device, k, positions, cos_sin, q_out, k_out, wq, wk)
-    args = (*_rows(q, "q", (T, Hq, D)), *_rows(k, "k", (T, Hk, D)), T, Hq, Hk, D, _weight(wq, "wq", D),
-            _weight(wk, "wk", D), eps, *_rope3(positions, cos_sin, T, interleaved),
-            *_rows(q_out, "q_out", (T, Hq, D)), *_rows(k_out, "k_out", (T, Hk, D)))
-    with guard:
-        _check("fp8_qk_norm_rope", lib.fp8_qk_norm_rope(*args, _stream_of(stream)))
-
-
-def _rope3(positions, cos_sin, T: int, interleaved: bool) -> tuple:
+    index = q.get_device()
+    _check_devices(index, k, positions, cos_sin, q_out, k_out, wq, wk)
     table, max_pos, R, pos = _rope(positions, cos_sin, T)
-    return table, max_pos, R, int(bool(interleaved)), pos
+    _call("fp8_qk_norm_rope", lib.fp8_qk_norm_rope, index, stream,
+          (*_rows(q, "q", shape), *_rows(k, "k", (T, Hk, D)), T, Hq, Hk, D, _weight(wq, "wq", D),
+           _weight(wk, "wk", D), eps, table, max_pos, R, 1 if interleaved else 0, pos,
+           *_rows(q_out, "q_out", shape), *_rows(k_out, "k_out", (T, Hk, D))))
 
 
 def fp8_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
@@ -220,26 +230,27 @@ def fp8_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
     outside the cache, such as -1, is skipped; they must differ) of the cache."""
     T = k.shape[0]
     shape = (T, cache.heads, cache.head_dim)
-    guard = _on(cache.device, k, v, slots)
-    args = (*_rows(k, "k", shape), *_rows(v, "v", shape), T, _vec(slots, "slots", T, torch.int64), cache._ref)
-    with guard:
-        _check("fp8_kv_write", lib.fp8_kv_write(*args, _stream_of(stream)))
+    index = cache.index
+    _check_devices(index, k, v, slots)
+    _call("fp8_kv_write", lib.fp8_kv_write, index, stream,
+          (*_rows(k, "k", shape), *_rows(v, "v", shape), T, _vec(slots, "slots", T, _I64), cache._ref))
 
 
 def fp8_qk_norm_rope_kv_write(q, k, v, positions, cos_sin, slots, cache: KVCache, q_out, wq=None, wk=None,
                               eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """fp8_qk_norm_rope and fp8_kv_write in one pass: q into q_out, k (quantised from fp32) and v
     into the cache."""
-    T, Hq, D = q.shape
+    T, Hq, D = q_shape = q.shape
     shape = (T, cache.heads, cache.head_dim)
     if D != cache.head_dim:
         raise ValueError(f"q has head dimension {D}, the cache {cache.head_dim}")
-    guard = _on(cache.device, q, k, v, positions, cos_sin, slots, q_out, wq, wk)
-    args = (*_rows(q, "q", (T, Hq, D)), *_rows(k, "k", shape), *_rows(v, "v", shape), T, Hq, _weight(wq, "wq", D),
-            _weight(wk, "wk", D), eps, *_rope3(positions, cos_sin, T, interleaved),
-            _vec(slots, "slots", T, torch.int64), cache._ref, *_rows(q_out, "q_out", (T, Hq, D)))
-    with guard:
-        _check("fp8_qk_norm_rope_kv_write", lib.fp8_qk_norm_rope_kv_write(*args, _stream_of(stream)))
+    index = cache.index
+    _check_devices(index, q, k, v, positions, cos_sin, slots, q_out, wq, wk)
+    table, max_pos, R, pos = _rope(positions, cos_sin, T)
+    _call("fp8_qk_norm_rope_kv_write", lib.fp8_qk_norm_rope_kv_write, index, stream,
+          (*_rows(q, "q", q_shape), *_rows(k, "k", shape), *_rows(v, "v", shape), T, Hq, _weight(wq, "wq", D),
+           _weight(wk, "wk", D), eps, table, max_pos, R, 1 if interleaved else 0, pos,
+           _vec(slots, "slots", T, _I64), cache._ref, *_rows(q_out, "q_out", q_shape)))
 
 
 def fp8_kv_read(cache: KVCache, table, offsets, k_out, v_out, stream=None) -> None:
@@ -248,23 +259,20 @@ def fp8_kv_read(cache: KVCache, table, offsets, k_out, v_out, stream=None) -> No
     offsets int32 [B + 1] on the device).  Rows outside every range are not written."""
     B = offsets.shape[0] - 1
     rows = k_out.shape[0]
-    guard = _on(cache.device, table, offsets, k_out, v_out)
+    index = cache.index
+    _check_devices(index, table, offsets, k_out, v_out)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _expect(t, (rows, cache.heads, cache.head_dim), n, torch.bfloat16)
+        _expect(t, (rows, cache.heads, cache.head_dim), n, _BF16)
         if not t.is_contiguous():
             raise ValueError(f"{n} must be contiguous")
-    args = (cache._ref, *_table(table, B), _vec(offsets, "offsets", B + 1, torch.int32), B, rows, k_out.data_ptr(),
-            v_out.data_ptr())
-    with guard:
-        _check("fp8_kv_read", lib.fp8_kv_read(*args, _stream_of(stream)))
+    _call("fp8_kv_read", lib.fp8_kv_read, index, stream,
+          (cache._ref, *_table(table, B), _vec(offsets, "offsets", B + 1, _I32), B, rows, k_out.data_ptr(),
+           v_out.data_ptr()))
 
 
 def paged_attention_ws_bytes(B: int, Hq: int, cache: KVCache) -> int:
     """Workspace of fp8_paged_attention for B sequences and Hq query heads, on the cache's device."""
-    guard = _NO_GUARD
-    if cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
-        guard = torch.cuda.device(cache.device)
-    with guard:
+    with torch.cuda.device(cache.index) if cache.index >= 0 else contextlib.nullcontext():
         n = lib.fp8_paged_attention_ws_bytes(B, Hq, cache._ref)
     if n == 0:
         raise ValueError(f"no attention of {Hq} query heads over this cache of {cache.heads} kv heads, "
@@ -279,24 +287,25 @@ def fp8_paged_attention(q, cache: KVCache, table, lens, out, workspace, lse=None
     [B, Hq, D], and the log of the softmax's sum in lse (fp32 [B, Hq]) when given.  scale:
     1 / sqrt(D) unless given.  workspace: paged_attention_ws_bytes(B, Hq, cache) bytes; calls that
     share it must be ordered on one stream."""
-    B, Hq, D = q.shape
+    B, Hq, D = shape = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q has head dimension {D}, the cache {cache.head_dim}")
-    guard = _on(cache.device, q, table, lens, out, workspace, lse)
-    qa = _rows(q, "q", (B, Hq, D))
-    _expect(out, (B, Hq, D), "out", torch.bfloat16)
+    index = cache.index
+    _check_devices(index, q, table, lens, out, workspace, lse)
+    if out.dtype is not _BF16:
+        raise TypeError(f"out has dtype {out.dtype}, expected torch.bfloat16")
+    if out.shape != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
     if not out.is_contiguous() or not workspace.is_contiguous():
         raise ValueError("out and workspace must be contiguous")
     if lse is not None:
-        _expect(lse, (B, Hq), "lse", torch.float32)
+        _expect(lse, (B, Hq), "lse", _F32)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
-    args = (*qa, B, Hq, cache._ref, *_table(table, B), _vec(lens, "lens", B, torch.int32),
-            1.0 / math.sqrt(D) if scale is None else scale, window, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-    with guard:
-        _check("fp8_paged_attention", lib.fp8_paged_attention(*args, _stream_of(stream)))
+    _call("fp8_paged_attention", lib.fp8_paged_attention, index, stream,
+          (*_rows(q, "q", shape), B, Hq, cache._ref, *_table(table, B), _vec(lens, "lens", B, _I32),
+           1.0 / math.sqrt(D) if scale is None else scale, window, out.data_ptr(),
+           None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes))
 
 
 # ------------------------------------------------------ allocating wrappers
