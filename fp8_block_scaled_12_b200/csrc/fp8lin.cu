@@ -314,20 +314,20 @@ int launch_tensor_quant(const uint16_t* x, int64_t n, uint8_t* q, float* s, cuda
 // of its heads of one token.
 constexpr int kCostBf16 = 4, kCostTurned = 7, kCostPlain = 4;
 
-template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
+template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
 int launch_norm_rope_write(KvWriteArgs a, cudaStream_t st) {
   constexpr int64_t groups = 256 / LPH;                  // groups of lanes per block
-  auto kern = k_norm_rope_write<LPH, ROPE, FMT, SF, CACHE>;
+  auto kern = k_norm_rope_write<LPH, U, ROPE, FMT, SF, CACHE>;
   static std::atomic<int> occ[64];
   const int64_t cap = int64_t(num_sms()) * resident_blocks(occ, kern, 256);
   int64_t work[3] = {0, 0, 0}, all = 0, blocks = 0;
   for (int i = 0; i < a.parts; ++i) {
     const KvPart& c = a.part[i];
-    work[i] = int64_t((c.heads + kWriteHeads - 1) / kWriteHeads) * (c.out ? kCostBf16 : (c.turn && a.R > 0) || c.w ? kCostTurned : kCostPlain);
+    work[i] = int64_t((c.heads + U - 1) / U) * (c.out ? kCostBf16 : (c.turn && a.R > 0) || c.w ? kCostTurned : kCostPlain);
     all += work[i];
   }
   for (int i = 0; i < a.parts; ++i) {
-    const int64_t u = (a.part[i].heads + kWriteHeads - 1) / kWriteHeads;
+    const int64_t u = (a.part[i].heads + U - 1) / U;
     int64_t n = (a.T * u + groups - 1) / groups;
     const int64_t share = cap * work[i] / all, least = (u + groups - 1) / groups;
     if (n > share) n = share;
@@ -337,6 +337,17 @@ int launch_norm_rope_write(KvWriteArgs a, cudaStream_t st) {
     blocks += n;
   }
   return cuda_status(launch(kern, unsigned(blocks), 256, 0, st, a));
+}
+
+// Heads per group of lanes: one while every group has a single token (64 tokens of 32 + 8 + 8
+// heads: 2.2 us against 3.1 us with two), two beyond (16384 tokens: 66 us against 91 us with one).
+template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
+int launch_norm_rope_write(const KvWriteArgs& a, cudaStream_t st) {
+  int64_t heads = 0;
+  for (int i = 0; i < a.parts; ++i) heads += a.part[i].heads;
+  return a.T * heads <= int64_t(num_sms()) * 3 * (256 / LPH)
+             ? launch_norm_rope_write<LPH, 1, ROPE, FMT, SF, CACHE>(a, st)
+             : launch_norm_rope_write<LPH, 2, ROPE, FMT, SF, CACHE>(a, st);
 }
 
 template <int ROPE, int FMT, int SF, bool CACHE>

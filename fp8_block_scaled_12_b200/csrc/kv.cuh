@@ -72,8 +72,8 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // LPH lanes own one head of one token, 16 channels each as two runs of 8 (a, b): for pairs
 // (i, R/2 + i) the two runs that rotate into each other, so that the rotation never leaves a
 // thread, else run j of each half of the head.  Loads and bf16 stores are 16 bytes a lane and
-// adjacent over the lanes.  A group of lanes keeps kWriteHeads heads and goes from token to
-// token: the norm's weights are loaded once, position, slot, cosines and sines serve all of its
+// adjacent over the lanes.  A group of lanes keeps U heads (two, or one while one token a group is all
+// there is: the heads' latencies add up then) and goes from token to token: the norm's weights are loaded once, position, slot, cosines and sines serve all of its
 // heads, nothing is divided but the slot, and the channels of the next kWriteAhead tokens are
 // on their way through shared memory meanwhile.  A block works on one of q, k and v, so
 // pointers and strides stay in constant memory and what one of them does not need is not there.
@@ -82,12 +82,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // one head a group 93 us, 8 channels a lane, scalar arithmetic and no loads ahead 133 us); the
 // same k and v alone: 21 us; norm and rotation of 4096 tokens of 32 + 8 heads: 16.3 us.
 constexpr int kWriteAhead = 2;
-constexpr int kWriteHeads = 2;
-typedef uint4 WriteRing[kWriteAhead + 1][kWriteHeads][2][256];
 
-template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
-__device__ __forceinline__ void write_part(const KvWriteArgs& a, const KvPart& c, WriteRing& ring) {
-  constexpr int U = kWriteHeads;
+template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
+__device__ __forceinline__ void write_part(const KvWriteArgs& a, const KvPart& c,
+                                           uint4 (&ring)[kWriteAhead + 1][U][2][256]) {
   const int units = (c.heads + U - 1) / U;
   const int j = threadIdx.x & (LPH - 1);
   const int group = ((int(blockIdx.x) - c.begin) * 256 + int(threadIdx.x)) / LPH;
@@ -262,19 +260,19 @@ __device__ __forceinline__ void write_part(const KvWriteArgs& a, const KvPart& c
 }
 
 // CACHE: whether any part goes into the cache.
-template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
+template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
 __global__ void __launch_bounds__(256, 3) k_norm_rope_write(const __grid_constant__ KvWriteArgs a) {
-  __shared__ WriteRing ring;
+  __shared__ uint4 ring[kWriteAhead + 1][U][2][256];
   pdl_wait();
   pdl_trigger();
   int i = 0;
   while (i + 1 < a.parts && int(blockIdx.x) >= a.part[i + 1].begin) ++i;
   const KvPart& c = a.part[i];
   if (!CACHE || c.out != nullptr) {
-    write_part<LPH, ROPE, FMT, SF, false>(a, c, ring);
+    write_part<LPH, U, ROPE, FMT, SF, false>(a, c, ring);
   } else if constexpr (CACHE) {
-    if (ROPE == kRopeNone || c.turn) write_part<LPH, ROPE, FMT, SF, true>(a, c, ring);
-    else write_part<LPH, kRopeNone, FMT, SF, true>(a, c, ring);
+    if (ROPE == kRopeNone || c.turn) write_part<LPH, U, ROPE, FMT, SF, true>(a, c, ring);
+    else write_part<LPH, U, kRopeNone, FMT, SF, true>(a, c, ring);
   }
 }
 
