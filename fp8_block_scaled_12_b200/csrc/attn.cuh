@@ -21,14 +21,15 @@
 //            most 2^-17 relative, or 2^-30 of the tile's largest possible w.  Each tile's
 //            product lands in fresh tensor-memory columns and is folded into fp32 registers
 //            (one channel d per thread) with the running maximum's factors.
-// A CTA (one per SM): warps 0 and 3 load pages (TMA; one lane per box of gcd(page, 128) rows)
-// and scales, warp 1 issues the score MMAs, warp 2 the output MMAs, and two warpgroups (warps
-// 4-11) do softmax and accumulation.  Each warpgroup works through a range of
-// tiles of its own; the loads and MMAs take one tile of each in turn.
+// A CTA (one per SM): two warpgroups (warps 4-11) do softmax and accumulation, each working
+// through a range of tiles of its own, for which one warp loads pages (TMA; one lane per box of
+// gcd(page, 128) rows) and scales and another issues the MMAs.  K and V of a tile are halves that
+// take slots of the warpgroup's own ring, K's free after the scores, V's after the outputs: the
+// warpgroups never wait for one another.
 //
 // Split: the batch's tiles, row after row (a row is a sequence, kv head and chunk of GT query
-// heads), form one list that is cut into equal ranges, one per warpgroup ("worker"), whatever
-// the lengths.  A row inside one range is finished there; a row cut by a border leaves partial
+// heads), form one list that is cut into ranges of equal cost, one per warpgroup ("worker"),
+// whatever the lengths.  A row inside one range is finished there; a row cut by a border leaves partial
 // sums (o, m, l) in the workspace, which k_attn_join adds up in the order of the tiles, so
 // results do not depend on timing.
 //
@@ -52,6 +53,9 @@ namespace fp8lin {
 
 constexpr int kAttnThreads = 384;
 constexpr int kAttnTile = 128;
+// Tiles whose scales are held: a K-slot is filled for tile j only after the outputs of tile j - 4
+// (or a later one) have left a V-slot, whatever the ring's length.
+constexpr int kScaleRing = 4;
 // Register split of the variant with 16 heads (the pool is kLaunchRegs a thread).
 constexpr uint32_t kAttnLoadRegs = 88, kAttnSoftmaxRegs = 208;
 static_assert(128 * kAttnLoadRegs + 256 * kAttnSoftmaxRegs <= 384 * kLaunchRegs, "register split exceeds pool");
@@ -78,43 +82,53 @@ struct AttnArgs {
 template <int GT_, int DCH_>
 struct AttnCfg {
   static constexpr int GT = GT_, DCH = DCH_;
-  static constexpr int STAGES = DCH == 2 ? 3 : GT == 8 ? 6 : 5;
-  static constexpr uint32_t KV_BYTES = kAttnTile * 128 * DCH;
+  static constexpr uint32_t KV_BYTES = kAttnTile * 128 * DCH;   // of K or V of one tile: a slot
+  // Slots of each warpgroup's ring.  More in flight do not help: with 6 of 16 KB the requests
+  // disturb one another (8 sequences of up to 64000 tokens: 108 us; 103 us with 5, 101 us with 4,
+  // 105 us with 3), with fewer the loads show as soon as the clock drops (64 sequences of up to
+  // 24000 tokens back to back for 80 ms: 252 us with 5, 258 us with 4, 280 us with 3).
+  static constexpr int SLOTS = DCH == 2 ? 3 : 5;
   static constexpr uint32_t Q_BYTES = 2 * GT * 128 * DCH;
   static constexpr uint32_t P_ROW = 4 * GT;                  // bytes per token of the split weights
   static constexpr uint32_t P_BYTES = kAttnTile * P_ROW;
-  static constexpr uint32_t OFF_Q = STAGES * 2 * KV_BYTES;
+  static constexpr uint32_t OFF_Q = 2 * SLOTS * KV_BYTES;
   static constexpr uint32_t OFF_P = OFF_Q + 4 * Q_BYTES;     // queries: two buffers a warpgroup
-  static constexpr uint32_t OFF_S = OFF_P + 2 * P_BYTES;     // scales: [STAGES][2][128] fp32
-  static constexpr uint32_t OFF_STATE = OFF_S + STAGES * 1024;
+  static constexpr uint32_t OFF_S = OFF_P + 2 * P_BYTES;     // scales: [warpgroup][kScaleRing][2][128] fp32
+  static constexpr uint32_t OFF_STATE = OFF_S + 2 * kScaleRing * 1024;
   static constexpr uint32_t S_COLS = 2 * GT, O_COLS = 4 * GT;
   static constexpr uint32_t TMEM_USED = 2 * (2 * S_COLS + DCH * O_COLS);     // two score buffers a warpgroup
   static constexpr uint32_t TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : 256;
 };
 
-template <int GT, int STAGES>
+// What a warpgroup has to know of the batch.
+struct AttnRange {
+  int tiles;                 // of the batch
+  int b, off, count;         // its first tile: sequence and place among its tiles; how many it takes
+};
+
+template <int GT, int SLOTS>
 struct alignas(16) AttnState {            // arrays [2]: by warpgroup
   float red[2][2][4][GT];  // [parity of its tile]: per-warp maxima
   float redsv[2][2][4];
   float lsum[2][4][GT];    // per-warp sums of p
   float cq[2][2][GT];      // per-head factor of the staged queries
-  uint64_t full[STAGES];   // pages
-  uint64_t scales[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[2][SLOTS];
+  uint64_t empty[2][SLOTS];
+  uint64_t scales[2][kScaleRing];
   uint64_t qfull[2][2];    // [buffer]
-  uint64_t sfull[2][2], sfree[2][2];       // [parity of its tile]
+  uint64_t sfull[2][2];    // [parity of its tile]
   uint64_t pfull[2], ofull[2];
   uint64_t drain[2];
-  uint32_t boxes[STAGES];  // which boxes of the stage hold a valid page
-  int seg[STAGES];         // its segment of the worker's range
+  uint32_t boxes[2][kScaleRing];           // which boxes of the tile hold a valid page
+  int seg[2][kScaleRing];                  // its segment of the worker's range
   uint32_t tmem_base;
   int abort;
-  int total, first_b[2], first_off[2];
+  AttnRange range[2];
 };
 
 template <class C>
 constexpr size_t attn_smem_bytes() {
-  return 1024 + C::OFF_STATE + sizeof(AttnState<C::GT, C::STAGES>);
+  return 1024 + C::OFF_STATE + sizeof(AttnState<C::GT, C::SLOTS>);
 }
 
 // Tokens [st, len) of a sequence, and its tiles [ft, ft + n): at least one, so that an empty
@@ -133,19 +147,24 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// The ranges of the list of tiles: worker k of n takes [total k / n, total (k + 1) / n).  Workers
-// of one CTA are grid.x apart, so few tiles spread over the SMs first.
+// The ranges of the list of tiles.  Where a worker has several tiles to take, each row counts
+// kAttnRowCost tiles more than it has, which stand before its first, for its queries, sums and
+// outputs (with equal tiles the workers of many short rows ended up
+// to 8 of 47 us after the others in a batch of 32 ragged sequences: 59 us in all, 57 us counting
+// one, 55.6 us two or three; 8 rows of 8 tiles, one a worker, take 8.0 us without and 9.1 us with the extra).
+// Worker k of n takes [total k / n, total (k + 1) / n) of this list.  Workers of one CTA are
+// grid.x apart, so few tiles spread over the SMs first.
+constexpr int kAttnRowCost = 2;
 struct AttnPlan {
-  int total, workers;
-  __device__ __forceinline__ AttnPlan(int total_) : total(total_), workers(min(2 * int(gridDim.x), total_)) {}
+  int tiles, workers, cost, total;
+  __device__ __forceinline__ AttnPlan(int tiles_, int rows) : tiles(tiles_) {
+    workers = min(2 * int(gridDim.x), tiles);
+    cost = tiles >= 4 * workers ? kAttnRowCost : 0;
+    total = tiles + cost * rows;
+  }
   __device__ __forceinline__ int begin(int k) const { return int(int64_t(total) * min(k, workers) / workers); }
   __device__ __forceinline__ int worker(int wg) const { return int(blockIdx.x) + wg * int(gridDim.x); }
-  __device__ __forceinline__ int count(int wg) const { return begin(worker(wg) + 1) - begin(worker(wg)); }
 };
-
-// Place in the CTA's sequence of loads of tile j of warpgroup g: the warpgroups take turns
-// while both have tiles.
-__device__ __forceinline__ int attn_place(int j, int g, int fewer) { return j < fewer ? 2 * j + g : j + fewer; }
 
 // The walk over a worker's range, tile by tile (next_tile) or segment by segment (a segment:
 // the part of one row inside the range).  Every role walks the same sequence.
@@ -281,32 +300,46 @@ __device__ __forceinline__ uint32_t split16(float& a, float& b) {
   return c;
 }
 
-// Scan of the batch by one warp: the number of tiles of all rows, then the sequence and the
-// offset in its rows at which the range of this CTA's warpgroup `wg` begins.
-__device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int wg, int* total, int* first_b,
-                                          int* first_off) {
+// Scan of the batch by one warp: the list's length, then the tiles at both ends of the range.
+__device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int wg, AttnRange* out) {
   const int rows = a.H * a.HC;
-  int sum = 0;
+  int tiles = 0;
   for (int i = 0; i < a.B; i += 32)
-    sum += __reduce_add_sync(~0u, i + lane < a.B ? attn_seq(a, i + lane).n * rows : 0);
-  const AttnPlan plan(sum);
-  const int x0 = plan.begin(plan.worker(wg));
-  int run = 0;
-  for (int i = 0; i < a.B && run <= x0; i += 32) {
-    const int v = i + lane < a.B ? attn_seq(a, i + lane).n * rows : 0;
-    int inc = v;
+    tiles += __reduce_add_sync(~0u, i + lane < a.B ? attn_seq(a, i + lane).n * rows : 0);
+  const AttnPlan plan(tiles, a.B * rows);
+  const int k = plan.worker(wg), x0 = plan.begin(k), x1 = plan.begin(k + 1);
+  int run = 0;                                             // tiles of the sequences before these 32
+  int first = 0, last = 0;                                 // numbers of the range's first tile and the next range's
+  if (lane == 0) {
+    out->tiles = tiles;
+    out->b = out->off = out->count = 0;
+  }
+  for (int i = 0; x0 < x1 && i < a.B; i += 32) {
+    const int n = i + lane < a.B ? attn_seq(a, i + lane).n : 0;
+    int inc = n * rows;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(~0u, inc, d);
       if (lane >= d) inc += y;
     }
-    if (x0 >= run + inc - v && x0 < run + inc) {
-      *first_b = i + lane;
-      *first_off = x0 - (run + inc - v);
+    const int before = run + inc - n * rows;               // tiles and list entries before this sequence
+    const int entry = before + plan.cost * (i + lane) * rows, per = n + plan.cost;
+    auto locate = [&](int x) {                             // place of list entry x among this sequence's tiles
+      const int row = (x - entry) / per;
+      return row * n + max(0, x - entry - row * per - plan.cost);
+    };
+    const bool has0 = n > 0 && x0 >= entry && x0 < entry + rows * per;
+    const bool has1 = n > 0 && x1 >= entry && x1 < entry + rows * per;
+    if (has0) {
+      out->b = i + lane;
+      out->off = locate(x0);
     }
+    first = __reduce_add_sync(~0u, has0 ? before + locate(x0) : 0) + first;
+    last = __reduce_add_sync(~0u, has1 ? before + locate(x1) : 0) + last;
     run += __shfl_sync(~0u, inc, 31);
   }
-  if (lane == 0) *total = sum;
+  __syncwarp();
+  if (lane == 0 && x0 < x1) out->count = (x1 == plan.total ? tiles : last) - first;
 }
 
 // Queries of a segment -> two E4M3 pieces as K-major rows (hi: head g, lo: head GT + g) in
@@ -391,8 +424,8 @@ template <int FMT, class C>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     k_paged_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const AttnArgs a) {
-  constexpr int GT = C::GT, DCH = C::DCH, STAGES = C::STAGES;
-  using State = AttnState<GT, STAGES>;
+  constexpr int GT = C::GT, DCH = C::DCH, SLOTS = C::SLOTS;
+  using State = AttnState<GT, SLOTS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -403,17 +436,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&ps->full[s]), 1);
-      mbar_init(smem_u32(&ps->scales[s]), 32);
-      mbar_init(smem_u32(&ps->empty[s]), 1);
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ps->qfull[i][0]), 4);
-      mbar_init(smem_u32(&ps->qfull[i][1]), 4);
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(smem_u32(&ps->sfull[i][k]), 1);
-        mbar_init(smem_u32(&ps->sfree[i][k]), 4);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(smem_u32(&ps->full[i][s]), 1);
+        mbar_init(smem_u32(&ps->empty[i][s]), 1);
+      }
+      for (int s = 0; s < kScaleRing; ++s) mbar_init(smem_u32(&ps->scales[i][s]), 1 + 32);   // `boxes`, copies
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(smem_u32(&ps->qfull[i][s]), 4);
+        mbar_init(smem_u32(&ps->sfull[i][s]), 1);
       }
       mbar_init(smem_u32(&ps->pfull[i]), 4);
       mbar_init(smem_u32(&ps->ofull[i]), 1);
@@ -429,29 +460,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  if (warp == 2 || warp == 3) attn_scan(a, lane, warp - 2, &ps->total, &ps->first_b[warp - 2], &ps->first_off[warp - 2]);
+  if (warp == 2 || warp == 3) attn_scan(a, lane, warp - 2, &ps->range[warp - 2]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ps->tmem_base;                 // scores of both warpgroups, then outputs
-  const AttnPlan plan(ps->total);
-  const int n0 = plan.count(0), n1 = plan.count(1);
-  const int fewer = min(n0, n1), more = max(n0, n1);
-
   // (8 heads fit the registers of an even split)
   if (warp < 4) {
     if constexpr (GT > 8) setmaxnreg_dec<kAttnLoadRegs>();
-    const int count = n0 + n1;
-    const int longer = n0 >= n1 ? 0 : 1;               // takes the tiles left when the turns are over
-    if (warp == 0 || warp == 3) {
+    const int g = warp & 1, n = ps->range[g].count;      // the warpgroup it works for
+    const uint32_t ring = base + uint32_t(g * SLOTS) * C::KV_BYTES;
+    if (warp < 2) {
       // ------------------------------------------------ pages and scales -> shared memory
-      // one warp for each warpgroup's tiles; a lane owns a box of the tile and the scales of
-      // four tokens (rows of a box come in multiples of eight)
-      const int g = warp == 0 ? 0 : 1, n = g == 0 ? n0 : n1;
-      int j = 0;
+      // a lane owns a box of the tile and the scales of four tokens (rows of a box come in
+      // multiples of eight)
+      int u = 0;                             // half tiles (K, then V) given a slot
       if (n > 0) {
         AttnWalk w;
-        w.start(a, ps->first_b[g], ps->first_off[g], n);
+        w.start(a, ps->range[g].b, ps->range[g].off, n);
         const int nb = kAttnTile / a.BR;
         const int sbox = lane * 4 / a.BR, srow = lane * 4 - sbox * a.BR;
         const int step_p = kAttnTile / a.P, step_r = kAttnTile - step_p * a.P;   // a tile further in pages and rows
@@ -470,8 +496,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           lookup();
         };
         enter();
-        for (; j < n; ++j) {
-          const int it = attn_place(j, g, fewer), s = it % STAGES;
+        for (int j = 0; j < n; ++j) {
           const int pg = page, rw = row, ch = h, sg = seg;
           if (j + 1 < n) {
             if (w.next_tile(a)) {
@@ -488,109 +513,139 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               lookup();
             }
           }
-          if (!attn_wait_warp(smem_u32(&ps->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, limit)) break;
           const bool ok = pg >= 0 && pg < a.pages;
-          const uint32_t bar = smem_u32(&ps->full[s]);
+          const int pc = ok ? pg : int(a.pages);
           const uint32_t boxes = __ballot_sync(~0u, ok);
+          const int64_t spage = __shfl_sync(~0u, pg, sbox);
+          const int sr = __shfl_sync(~0u, rw, sbox) + srow;
+          int s = u % SLOTS;
+          if (!attn_wait_warp(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
+          const int e = j % kScaleRing;
           if (lane == 0) {
-            ps->boxes[s] = boxes;
-            ps->seg[s] = sg;
-            mbar_arrive_expect_tx(bar, 2 * C::KV_BYTES);
+            ps->boxes[g][e] = boxes;
+            ps->seg[g][e] = sg;
+            mbar_arrive(smem_u32(&ps->scales[g][e]));
+            mbar_arrive_expect_tx(smem_u32(&ps->full[g][s]), C::KV_BYTES);
           }
           __syncwarp();
           if (lane < nb) {
-            const uint32_t off = base + uint32_t(s) * (2 * C::KV_BYTES) + uint32_t(lane * a.BR) * 128u;
-            const int pc = ok ? pg : int(a.pages);
 #pragma unroll
-            for (int c = 0; c < DCH; ++c) {
-              tma_load_4d(off + c * (kAttnTile * 128), &tmK, bar, c * 128, rw, ch, pc);
-              tma_load_4d(off + C::KV_BYTES + c * (kAttnTile * 128), &tmV, bar, c * 128, rw, ch, pc);
-            }
+            for (int c = 0; c < DCH; ++c)
+              tma_load_4d(ring + s * C::KV_BYTES + c * (kAttnTile * 128) + uint32_t(lane * a.BR) * 128u, &tmK,
+                          smem_u32(&ps->full[g][s]), c * 128, rw, ch, pc);
           }
-          const int64_t spage = __shfl_sync(~0u, pg, sbox);
-          const int sr = __shfl_sync(~0u, rw, sbox) + srow;
           if ((boxes >> sbox) & 1u) {
             const int64_t at = (spage * a.H + ch) * a.P + sr;
-            const uint32_t sc = base + C::OFF_S + s * 1024 + lane * 16;
+            const uint32_t sc = base + C::OFF_S + (g * kScaleRing + e) * 1024 + lane * 16;
             cp_async16(sc, a.ks + at);
             cp_async16(sc + 512, a.vs + at);
           }
-          cp_async_arrive(smem_u32(&ps->scales[s]));
+          cp_async_arrive(smem_u32(&ps->scales[g][e]));
+          ++u;
+          s = u % SLOTS;
+          if (!attn_wait_warp(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&ps->full[g][s]), C::KV_BYTES);
+          __syncwarp();
+          if (lane < nb) {
+#pragma unroll
+            for (int c = 0; c < DCH; ++c)
+              tma_load_4d(ring + s * C::KV_BYTES + c * (kAttnTile * 128) + uint32_t(lane * a.BR) * 128u, &tmV,
+                          smem_u32(&ps->full[g][s]), c * 128, rw, ch, pc);
+          }
+          ++u;
         }
       }
       if (*abort) {                      // every load already issued lands before the CTA exits
-        for (int i = max(0, j - STAGES); i < j; ++i) {
-          const int it = attn_place(i, g, fewer);
-          mbar_drain(smem_u32(&ps->full[it % STAGES]), (it / STAGES) & 1u);
-        }
+        for (int i = max(0, u - SLOTS); i < u; ++i) mbar_drain(smem_u32(&ps->full[g][i % SLOTS]), (i / SLOTS) & 1u);
         cp_async_wait_all();
       }
       if (warp == 0) pdl_trigger();
-    } else if (warp == 1) {
-      // ------------------------------------------------ scores
-      // (the whole warp walks, one elected lane issues: operands then stay in uniform registers)
-      constexpr uint32_t id_s = attn_idesc(FMT, 2 * GT, false);
+    } else {
+      // ------------------------------------------------ MMAs
+      // the whole warp walks, one elected lane issues: operands then stay in uniform registers
+      constexpr uint32_t id_s = attn_idesc(FMT, 2 * GT, false), id_o = attn_idesc(FMT, 4 * GT, true);
       const int steps = (a.D + 31) / 32;
-      const uint32_t klo = attn_desc_lo(base), qlo = attn_desc_lo(base + C::OFF_Q);
-      for (int it = 0; it < count; ++it) {
-        const int s = it % STAGES;
-        const int g = it < 2 * fewer ? it & 1 : longer, j = it < 2 * fewer ? it >> 1 : it - fewer;
-        // the tile; the score buffer, read by the warpgroup two tiles ago; the queries
-        if (!attn_wait_warp(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort, limit)) break;
-        const int par = j & 1;
-        if (j > 1 && !attn_wait_warp(smem_u32(&ps->sfree[g][par]), ((j >> 1) & 1u) ^ 1u, abort, limit)) break;
-        const int seg = ps->seg[s];
-        if (!attn_wait_warp(smem_u32(&ps->qfull[g][seg & 1]), (seg >> 1) & 1u, abort, limit)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t k0 = klo + uint32_t(s) * (2 * C::KV_BYTES / 16);
-          const uint32_t q0 = qlo + uint32_t(2 * g + (seg & 1)) * (C::Q_BYTES / 16);
+      const uint32_t rlo = attn_desc_lo(ring);
+      const uint32_t qlo = attn_desc_lo(base + C::OFF_Q + 2 * g * C::Q_BYTES);
+      const uint32_t plo = attn_desc_lo(base + C::OFF_P + g * C::P_BYTES);
+      const uint32_t tmem_s = tmem + 2 * g * C::S_COLS, tmem_o = tmem + 4 * C::S_COLS + g * (DCH * C::O_COLS);
+      // Whichever product's operands are there goes first: in tile order, outputs whose weights
+      // are ready would wait for a later tile's K and keep V's slot meanwhile.  Scores run up to two tiles ahead of the outputs:
+      // the scores of tile j - 2 were read before its weights were announced.
+      auto ready = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(~0u, mbar_test_wait(smem_u32(bar), parity)) != 0;
+      };
+      bool ok = true;
+      uint32_t polls = 0;
+      uint64_t since = 0;
+      for (int js = 0, jo = 0; jo < n;) {
+        if (js < n && js <= jo + 1) {
+          const int u = 2 * js, s = u % SLOTS, par = js & 1;
+          if (ready(&ps->full[g][s], (u / SLOTS) & 1u)) {
+            const int seg = ps->seg[g][js % kScaleRing];
+            if (ready(&ps->qfull[g][seg & 1], (seg >> 1) & 1u)) {
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t k0 = rlo + uint32_t(s) * (C::KV_BYTES / 16);
+                const uint32_t q0 = qlo + uint32_t(seg & 1) * (C::Q_BYTES / 16);
 #pragma unroll
-          for (int k = 0; k < 4 * DCH; ++k)
-            if (k < steps)
-              mma_f8(tmem + (2 * g + par) * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
-                     attn_desc(q0 + (k / 4) * (2 * GT * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&ps->sfull[g][par]));
+                for (int k = 0; k < 4 * DCH; ++k)
+                  if (k < steps)
+                    mma_f8(tmem_s + par * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
+                           attn_desc(q0 + (k / 4) * (2 * GT * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
+                mma_commit(smem_u32(&ps->sfull[g][par]));
+                mma_commit(smem_u32(&ps->empty[g][s]));
+              }
+              __syncwarp();
+              ++js;
+              polls = 0;
+            }
+          }
         }
-        __syncwarp();
+        if (jo < js && ready(&ps->pfull[g], jo & 1u)) {
+          const int u = 2 * jo + 1, s = u % SLOTS;
+          if (ready(&ps->full[g][s], (u / SLOTS) & 1u)) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t v0 = rlo + uint32_t(s) * (C::KV_BYTES / 16);
+#pragma unroll
+              for (int c = 0; c < DCH; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_f8(tmem_o + c * C::O_COLS, attn_desc(v0 + c * (kAttnTile * 8) + k * (32 * 8), 128),
+                         attn_desc(plo + k * (2 * C::P_ROW), C::P_ROW), id_o, k > 0 ? 1u : 0u);
+              mma_commit(smem_u32(&ps->ofull[g]));
+              mma_commit(smem_u32(&ps->empty[g][s]));
+            }
+            __syncwarp();
+            ++jo;
+            polls = 0;
+          }
+        }
+        // the wait's bounds, as in mbar_wait
+        if ((++polls & 63u) == 0u || (limit < 1000 && polls > 1)) {
+          const uint64_t now = globaltimer_ns();
+          if (polls <= 64u) since = now;
+          const bool out = limit < 1000 || now - since > limit || polls > FP8LIN_WAIT_ITERS;
+          if (out && lane == 0) {
+            *abort = 1;
+            atomicOr(&g_device_error, 1u);
+          }
+          ok = !__any_sync(~0u, out || *abort);
+          if (!ok) break;
+        }
       }
+      for (int u = max(0, 2 * n - 2); ok && u < 2 * n; ++u)       // the last commits have arrived
+        ok = attn_wait_warp(smem_u32(&ps->empty[g][u % SLOTS]), (u / SLOTS) & 1u, abort, limit);
       if (*abort && lane == 0) {           // the MMAs already issued finish before tensor memory is freed
-        mma_commit(smem_u32(&ps->drain[0]));
-        mbar_drain(smem_u32(&ps->drain[0]), 0u);
-      }
-    } else if (warp == 2) {
-      // ------------------------------------------------ outputs
-      constexpr uint32_t id_o = attn_idesc(FMT, 4 * GT, true);
-      const uint32_t vlo = attn_desc_lo(base + C::KV_BYTES), plo = attn_desc_lo(base + C::OFF_P);
-      for (int it = 0; it < count; ++it) {
-        const int s = it % STAGES;
-        const int g = it < 2 * fewer ? it & 1 : longer, j = it < 2 * fewer ? it >> 1 : it - fewer;
-        if (!attn_wait_warp(smem_u32(&ps->pfull[g]), j & 1u, abort, limit)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t v0 = vlo + uint32_t(s) * (2 * C::KV_BYTES / 16);
-          const uint32_t p0 = plo + uint32_t(g) * (C::P_BYTES / 16);
-          const uint32_t o0 = tmem + 4 * C::S_COLS + g * (DCH * C::O_COLS);
-#pragma unroll
-          for (int c = 0; c < DCH; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f8(o0 + c * C::O_COLS, attn_desc(v0 + c * (kAttnTile * 8) + k * (32 * 8), 128),
-                     attn_desc(p0 + k * (2 * C::P_ROW), C::P_ROW), id_o, k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&ps->ofull[g]));
-          mma_commit(smem_u32(&ps->empty[s]));
-        }
-        __syncwarp();
-      }
-      if (*abort && lane == 0) {
-        mma_commit(smem_u32(&ps->drain[1]));
-        mbar_drain(smem_u32(&ps->drain[1]), 0u);
+        mma_commit(smem_u32(&ps->drain[g]));
+        mbar_drain(smem_u32(&ps->drain[g]), 0u);
       }
     }
   } else {
     if constexpr (GT > 8) setmaxnreg_inc<kAttnSoftmaxRegs>();
     const int wg = (warp - 4) >> 2;
-    const int mine = wg == 0 ? n0 : n1;
+    const int mine = ps->range[wg].count;
     if (mine > 0) {
       // ------------------------------------------------ softmax and accumulation
       const int quad = warp & 3;                   // tensor-memory lanes of this warp
@@ -598,9 +653,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t tlane = uint32_t(quad * 32) << 16;
       const uint32_t tmem_s = tmem + tlane + 2 * wg * C::S_COLS;
       const uint32_t tmem_o = tmem + tlane + 4 * C::S_COLS + wg * (DCH * C::O_COLS);
+      const AttnPlan plan(ps->range[wg].tiles, a.B * a.H * a.HC);
       const int worker = plan.worker(wg);
       AttnWalk w;
-      w.start(a, ps->first_b[wg], ps->first_off[wg], mine);
+      w.start(a, ps->range[wg].b, ps->range[wg].off, mine);
       AttnWalk ahead = w;                          // the next segment whose queries are staged
       AttnQuery<C> qn;
       auto stage = [&](int buf) {
@@ -655,12 +711,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int t_first = w.t;
         bool failed = false;
         for (int t = t_first; t < w.t1; ++t, ++j) {
-          const int it = attn_place(j, wg, fewer), s = it % STAGES, par = j & 1;
-          ok &= attn_wait(smem_u32(&ps->full[s]), (it / STAGES) & 1u, abort, limit);
-          ok &= attn_wait(smem_u32(&ps->scales[s]), (it / STAGES) & 1u, abort, limit);
-          const float* sc = reinterpret_cast<const float*>(gbase + C::OFF_S + s * 1024);
+          const int par = j & 1, e = j % kScaleRing;
+          ok &= attn_wait(smem_u32(&ps->scales[wg][e]), (j / kScaleRing) & 1u, abort, limit);
+          const float* sc = reinterpret_cast<const float*>(gbase + C::OFF_S + (wg * kScaleRing + e) * 1024);
           const int t0 = (w.s.ft + t) * kAttnTile;
-          const uint32_t boxes = ps->boxes[s];
+          const uint32_t boxes = ps->boxes[wg][e];
           const bool live = t0 + tok >= w.s.st && t0 + tok < w.s.len && ((boxes >> (tok / a.BR)) & 1u);
           const float sk = live ? sc[tok] : 0.0f, sv = live ? sc[128 + tok] : 0.0f;
           ok &= attn_wait(smem_u32(&ps->sfull[wg][par]), (j >> 1) & 1u, abort, limit);
@@ -672,9 +727,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             else tmem_ld32(tmem_s + par * C::S_COLS, r);
             tmem_ld_wait();
             tmem_regs_ready(r);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ps->sfree[wg][par]));
             float wm[GT];
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
@@ -734,7 +786,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             *reinterpret_cast<uint4*>(pr + ((i ^ sw) * 16)) =
                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           if (!live && ((boxes >> (tok / a.BR)) & 1u)) {        // whatever the cache holds there times 0 is 0
-            uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(s) * (2 * C::KV_BYTES) + C::KV_BYTES + tok * 128);
+            const int u = 2 * j + 1, s = u % SLOTS;
+            ok &= attn_wait(smem_u32(&ps->full[wg][s]), (u / SLOTS) & 1u, abort, limit);
+            uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(wg * SLOTS + s) * C::KV_BYTES + tok * 128);
 #pragma unroll
             for (int c = 0; c < DCH; ++c)
 #pragma unroll
@@ -796,8 +850,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (t_first == 0 && tok == 0) {
           int2 info = make_int2(-1, -1);
           if (!whole) {                            // the worker whose range holds the row's last tile
-            const int64_t last = int64_t(plan.begin(worker)) + j - w.t1 + w.s.n - 1;
-            info = make_int2(slot, int(((last + 1) * plan.workers + plan.total - 1) / plan.total) - 1);
+            const int64_t next = int64_t(plan.begin(worker + 1)) + w.s.n - w.t1;     // of the list: the next row
+            info = make_int2(slot, int((next * plan.workers + plan.total - 1) / plan.total) - 1);
           }
           a.ws_row[(int64_t(w.b) * a.H + w.c) * a.HC + w.hc] = info;
         }

@@ -945,7 +945,8 @@ int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B,
   const int64_t G = Hq / H, HC = attn_chunks(G, D);
   if (B > INT32_MAX || Hq > 65535 || B * H * HC > INT32_MAX) return FP8_ERR_SHAPE;
   if (max_pages > INT32_MAX / P || max_pages * P > INT32_MAX - 2 * kAttnTile) return FP8_ERR_SHAPE;
-  const int64_t tiles = B * H * HC * ((max_pages * P + kAttnTile - 1) / kAttnTile + 1);
+  // (the list of tiles counts in 32 bits)
+  const int64_t tiles = B * H * HC * ((max_pages * P + kAttnTile - 1) / kAttnTile + 1 + kAttnRowCost);
   if (tiles > INT32_MAX) return FP8_ERR_SHAPE;
   if (B == 0) return FP8_OK;
   if ((max_pages > 0 && !table) || !lens || !out || !workspace) return FP8_ERR_INVALID_ARG;
