@@ -77,6 +77,7 @@ struct AttnArgs {
   int64_t pages;
   float scale;
   int B, H, G, HC, D, P, BR;   // HC chunks of query heads per kv head; BR rows per box
+  int slots;               // partial sums that the workspace holds
 };
 
 template <int GT_, int DCH_>
@@ -882,7 +883,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const AttnArgs a) {
   pdl_wait();
   const int64_t row = blockIdx.x;
   const int2 info = a.ws_row[row];
-  if (info.x < 0) return;
+  // a whole row, or, after a wait that ran out, an entry that was never written
+  if (info.x < 0 || info.x >= a.slots || info.y < info.x / 2 || info.y >= a.slots / 2) return;
   const int g = blockIdx.y, hc = int(row % a.HC);
   if (hc * GT + g >= a.G) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

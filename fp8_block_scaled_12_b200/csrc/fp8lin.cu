@@ -404,9 +404,10 @@ inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1
 // Workspace of the attention: two partial sums for each of two workers an SM, then one entry
 // per row.
 struct AttnWs {
-  int64_t o, ml, row, total;
+  int64_t slots, o, ml, row, total;
   AttnWs(int64_t B, int64_t H, int64_t G, int64_t D) {
-    const int64_t slots = 4 * int64_t(num_sms()), gt = attn_gt(G, D);
+    const int64_t gt = attn_gt(G, D);
+    slots = 4 * int64_t(num_sms());
     o = 0;
     ml = o + slots * gt * D * 4;
     row = ml + slots * 2 * gt * 4;
@@ -978,6 +979,7 @@ int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B,
   a.q_row = q_row, a.q_head = q_head, a.table_stride = table_stride;
   a.window = window, a.cap = max_pages * P, a.pages = cache->num_pages, a.scale = scale;
   a.B = int(B), a.H = int(H), a.G = int(G), a.HC = int(HC), a.D = int(D), a.P = int(P), a.BR = int(br);
+  a.slots = int(ws.slots);
   const int grid = int(tiles < num_sms() ? tiles : num_sms());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cache->fmt == FP8_E4M3 ? launch_attention<kE4M3>(mk, mv, a, grid, st)

@@ -90,6 +90,16 @@ def test_rows_cut_by_the_ranges(cuda_device):
     case([5000, 1, 3000 - 1, 130, 12000, 0, 260, 7777], 4, 8, 128, 16, seed=5)
 
 
+@pytest.mark.parametrize("H,G,D,P", [(8, 4, 128, 16), (4, 12, 64, 32), (4, 4, 256, 64)])
+def test_many_tiles_a_worker(cuda_device, H, G, D, P):
+    """Ragged rows over the whole GPU, several tiles and several rows a worker, the two
+    warpgroups of a CTA with unequal shares."""
+    lens = [max(1, 6000 - int(6000 * ((0.6180339887498949 * i) % 1.0))) for i in range(40)]
+    c, table, q, n, out = case(lens, H, G, D, P, seed=11)
+    for _ in range(3):
+        assert torch.equal(F.paged_attention(q, c, table, n), out)
+
+
 @pytest.mark.parametrize("gain", [1e-3, 30.0, 300.0])
 def test_flat_and_peaked_softmax(cuda_device, gain):
     """Scores from almost equal to hundreds of nats apart."""
