@@ -369,9 +369,10 @@ int launch_cache_write(const KvWriteArgs& a, int fmt, int scale_fmt, cudaStream_
 template <int FMT>
 int launch_kv_read(KvReadArgs a, cudaStream_t st) {
   static std::atomic<int> occ[64];
-  const int64_t warps = int64_t(num_sms()) * resident_blocks(occ, k_kv_read<FMT>, 256) * 8;
-  a.run = int((a.rows + warps - 1) / warps);
-  const int64_t blocks = ((a.rows + a.run - 1) / a.run + 7) / 8;
+  const int64_t most = int64_t(num_sms()) * resident_blocks(occ, k_kv_read<FMT>, 256);
+  a.run = int((a.rows + most - 1) / most);
+  if (a.run < 8) a.run = 8;                              // a row a warp
+  const int64_t blocks = (a.rows + a.run - 1) / a.run;
   return cuda_status(launch(k_kv_read<FMT>, unsigned(blocks), 256, 0, st, a));
 }
 

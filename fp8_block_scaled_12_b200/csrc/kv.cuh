@@ -277,13 +277,14 @@ __global__ void __launch_bounds__(256, 3) k_norm_rope_write(const __grid_constan
 }
 
 // ------------------------------------------------------------------- read back
-// Row r of the outputs is token r - offsets[b] of the sequence b whose range holds r.  A warp
-// takes a run of rows, so that it searches the offsets once and reads the table once a page;
-// its steps are slices of 128 16-channel chunks of a row (k's heads, then v's), four chunks a
+// Row r of the outputs is token r - offsets[b] of the sequence b whose range holds r.  A block
+// takes a run of rows, its warps in turns, so that what it reads and writes at a time lies
+// together; a warp searches the offsets once and reads the table once a page.  Its steps are slices of 128 16-channel chunks of a row (k's heads, then v's), four chunks a
 // lane, and the next step's codes are loaded before this one's are converted.  Rows whose page
 // is not in the cache are zeros; rows outside every range are not written.
 // Bound by memory, two thirds of it the bf16 stores: 32 contexts of up to 4096 tokens, 8 heads
-// of 128: 79 us, 5.3 TB/s (92 us with two 16-byte stores in place of one of 32 bytes).
+// of 128: 74 us, 5.5 TB/s (92 us with two 16-byte stores in place of one of 32 bytes, 79 us with
+// runs of rows per warp).
 struct KvReadArgs {
   KvCache c;
   const int32_t* table;     // [B][max_pages]
@@ -293,7 +294,7 @@ struct KvReadArgs {
   int64_t table_stride, max_pages, rows;
   int B;
   uint32_t cph_magic;       // ceil(2^32 / (D / 16)): quotients by multiplication; 0 for D = 16
-  int run;                  // rows per warp
+  int run;                  // rows per block
 };
 
 // 4 codes -> 4 fp32 values times s, as two bf16 pairs.
@@ -320,15 +321,15 @@ __device__ __forceinline__ void store32(void* p, uint2 a, uint2 b, uint2 c, uint
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(256) k_kv_read(const KvReadArgs a) {
+__global__ void __launch_bounds__(256, 2) k_kv_read(const KvReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int cph = a.c.D / 16;                 // chunks per head
   const int chunks = a.c.H * cph;             // of k, and as many of v
-  const int64_t warp = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  int64_t r = max(warp * a.run, int64_t(__ldg(a.offsets)));
-  const int64_t end = min(min((warp + 1) * a.run, a.rows), int64_t(__ldg(a.offsets + a.B)));
+  const int64_t first_row = max(int64_t(blockIdx.x) * a.run, int64_t(__ldg(a.offsets)));
+  const int64_t end = min(min((int64_t(blockIdx.x) + 1) * a.run, a.rows), int64_t(__ldg(a.offsets + a.B)));
+  int64_t r = first_row + (threadIdx.x >> 5);
   if (r >= end) return;
   int b = 0;                                  // offsets[b] <= r < offsets[b + 1]
   for (int hi = a.B; hi - b > 1;) {
@@ -379,14 +380,18 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvReadArgs a) {
     first += 128;
     if (first >= 2 * chunks) {                // the next row
       first = 0;
-      if (++r < end) {
-        if (r >= next_b) {                    // the next sequence that has a row
+      r += 8;
+      row += 8;
+      if (r < end) {
+        if (r >= next_b) {                    // the sequence that has this row
           do next_b = __ldg(a.offsets + ++b + 1);
           while (r >= next_b);
-          pi = row = 0;
+          tok = int(r - __ldg(a.offsets + b));
+          pi = tok / a.c.P;
+          row = tok - pi * a.c.P;
           turn();
-        } else if (++row == a.c.P) {
-          row = 0;
+        } else if (row >= a.c.P) {            // pages hold at least eight rows
+          row -= a.c.P;
           ++pi;
           turn();
         }
