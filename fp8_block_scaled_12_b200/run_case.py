@@ -6,6 +6,8 @@
     python -m fp8_block_scaled_12_b200.run_case --op grouped --tokens 4096 --E 256 --N 2048 --K 7168
     python -m fp8_block_scaled_12_b200.run_case --op mx_gemm --M 4096 --N 28672 --K 8192 --scale ue8m0
     python -m fp8_block_scaled_12_b200.run_case --op mx_quant --M 16384 --K 7168
+    python -m fp8_block_scaled_12_b200.run_case --op attention --B 32 --len 8192 --Hq 32 --Hkv 8 --D 128 --page 16
+    python -m fp8_block_scaled_12_b200.run_case --op kv_fused --tokens 16384 --Hq 32 --Hkv 8 --D 128
 
 Inputs are prepared before the measured launches (so a profiler can skip them by
 launch count: the op's own launches come last, `--iters` of them, after `--warm`
@@ -42,10 +44,65 @@ def timed(fn, warm, iters):
     return a.elapsed_time(b) / max(iters, 1)
 
 
+def run_cache_op(a, fmt, sf, dev):
+    """The operators around the paged cache, on one projection's output per token."""
+    H, Hq, D, P = a.Hkv, a.Hq, a.D, a.page
+
+    def projected(n, seed):
+        x = synth.activations(n, (Hq + 2 * H) * D, seed=seed, device=dev).view(n, Hq + 2 * H, D)
+        return x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:]
+
+    if a.op in ("norm_rope", "kv_write", "kv_fused"):
+        T = a.tokens
+        q, k, v = projected(T, 0)
+        w = torch.ones(D, dtype=torch.bfloat16, device=dev)
+        pos = torch.arange(T, device=dev)
+        cs = F.rope_table(T, D, device=dev)
+        cache = F.KVCache(-(-T // P), P, H, D, fmt, sf, a.layout, dev)
+        qo = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        ko = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        if a.op == "norm_rope":
+            ms = timed(lambda: F.fp8_qk_norm_rope(q, k, pos, cs, qo, ko, w, w), a.warm, a.iters)
+            b = T * (Hq + H) * D * 4
+        elif a.op == "kv_write":
+            ms = timed(lambda: F.fp8_kv_write(k, v, pos, cache), a.warm, a.iters)
+            b = 2 * T * H * (D * 3 + 4)
+        else:
+            ms = timed(lambda: F.fp8_qk_norm_rope_kv_write(q, k, v, pos, cs, pos, cache, qo, w, w), a.warm, a.iters)
+            b = T * Hq * D * 4 + 2 * T * H * (D * 3 + 4)
+        print(f"{a.op} T={T} Hq={Hq} Hkv={H} D={D} page={P} {a.fmt}/{a.scale}: {ms * 1e3:.2f} us  {b / ms / 1e6:.1f} GB/s")
+        return
+    lens = [a.len if i % 2 == 0 else max(1, a.len // 2) for i in range(a.B)]
+    width = -(-a.len // P)
+    cache = F.KVCache(a.B * width, P, H, D, fmt, sf, a.layout, dev)
+    g = torch.Generator(device=dev).manual_seed(0)
+    table = torch.randperm(a.B * width, generator=g, device=dev).int().view(a.B, width)
+    for i, n in enumerate(lens):                       # every sequence's tokens, written as a prompt's are
+        _, k, v = projected(n, i)
+        tok = torch.arange(n, device=dev)
+        F.fp8_kv_write(k, v, table[i][tok // P].long() * P + tok % P, cache)
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    seen = sum(min(m, a.window or m) for m in lens) if a.op == "attention" else sum(lens)
+    b = 2 * seen * H * (D + 4)
+    if a.op == "kv_read":
+        off = torch.cat([torch.zeros(1, dtype=torch.int32, device=dev), n.cumsum(0).int()])
+        ko, vo = (torch.empty((sum(lens), H, D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        ms = timed(lambda: F.fp8_kv_read(cache, table, off, ko, vo), a.warm, a.iters)
+        b += 4 * seen * H * D
+    else:
+        q = synth.activations(a.B, Hq * D, seed=99, device=dev).view(a.B, Hq, D)
+        out = torch.empty_like(q)
+        ws = torch.empty(F.paged_attention_ws_bytes(a.B, Hq, cache), dtype=torch.uint8, device=dev)
+        ms = timed(lambda: F.fp8_paged_attention(q, cache, table, n, out, ws, window=a.window), a.warm, a.iters)
+    print(f"{a.op} B={a.B} len={a.len} Hq={Hq} Hkv={H} D={D} page={P} {a.layout} {a.fmt}: {ms * 1e3:.2f} us  "
+          f"{b / ms / 1e6:.1f} GB/s")
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", required=True, choices=["act_quant", "weight_quant", "gemm", "grouped", "mx_quant",
-                                                    "mx_gemm", "delayed", "gemm_quant", "dequant", "moe"])
+                                                    "mx_gemm", "delayed", "gemm_quant", "dequant", "moe",
+                                                    "norm_rope", "kv_write", "kv_fused", "kv_read", "attention"])
     ap.add_argument("--M", type=int, default=4096)
     ap.add_argument("--N", type=int, default=28672)
     ap.add_argument("--K", type=int, default=8192)
@@ -57,6 +114,14 @@ def main():
     ap.add_argument("--scale", choices=["fp32", "ue8m0"], default="fp32")
     ap.add_argument("--out", choices=["bf16", "fp32"], default="bf16")
     ap.add_argument("--dist", choices=["normal", "t3"], default="normal")
+    ap.add_argument("--B", type=int, default=32, help="sequences (kv_read, attention)")
+    ap.add_argument("--len", type=int, default=4096, help="their length; odd sequences have half of it")
+    ap.add_argument("--Hq", type=int, default=32)
+    ap.add_argument("--Hkv", type=int, default=8)
+    ap.add_argument("--D", type=int, default=128)
+    ap.add_argument("--page", type=int, default=64)
+    ap.add_argument("--layout", choices=["HND", "NHD"], default="HND")
+    ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--warm", type=int, default=1)
     a = ap.parse_args()
@@ -65,7 +130,9 @@ def main():
     sf = F.SCALE_FP32 if a.scale == "fp32" else F.SCALE_UE8M0
     odt = torch.bfloat16 if a.out == "bf16" else torch.float32
 
-    if a.op == "act_quant":
+    if a.op in ("norm_rope", "kv_write", "kv_fused", "kv_read", "attention"):
+        run_cache_op(a, fmt, sf, dev)
+    elif a.op == "act_quant":
         x = synth.activations(a.M, a.K, seed=0, dist=a.dist, device=dev)
         q = torch.empty((a.M, a.K), dtype=torch.uint8, device=dev)
         s = torch.empty((a.M, (a.K + 127) // 128), dtype=torch.float32, device=dev)

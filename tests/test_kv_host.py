@@ -208,3 +208,24 @@ def test_rope_table_angles_keep_far_positions():
             a = p * 10000.0 ** (-2 * i / 64)
             assert abs(float(t[p, i]) - math.cos(a)) < 1e-7
             assert abs(float(t[p, 32 + i]) - math.sin(a)) < 1e-7
+
+
+def test_c_client_and_structure_layout(tmp_path):
+    """A C99 program built against the header; the binding's structure has the same layout."""
+    import os
+    import shutil
+    import subprocess
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no C compiler")
+    here = os.path.dirname(os.path.abspath(__file__))
+    libdir = os.path.dirname(F.LIB_PATH)
+    exe = str(tmp_path / "c_kv_check")
+    subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", "-I",
+                    os.path.join(os.path.dirname(here), "include"), "-o", exe, os.path.join(here, "c_kv_check.c"),
+                    "-L", libdir, "-lfp8lin", "-Wl,-rpath," + libdir], check=True, capture_output=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
+    s = _CacheStruct
+    assert [int(x) for x in r.stdout.split()] == [ctypes.sizeof(s), s.v_scale.offset, s.num_pages.offset,
+                                                  s.token_stride.offset, s.scale_fmt.offset]
