@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               x[g] = live ? v : -INFINITY;
               wm[g] = warp_max(x[g]);
             }
-            const float wv = warp_max(sv);
+            const float wv = warp_max(fabsf(sv));
             if (lane == 0) {
 #pragma unroll
               for (int g = 0; g < GT; g += 4)

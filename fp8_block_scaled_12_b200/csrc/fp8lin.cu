@@ -482,6 +482,15 @@ int check_rows(const void* p, int64_t heads, int64_t tok, int64_t head, int64_t 
   return FP8_OK;
 }
 
+// The same for an output, whose tokens and heads must not overlap.
+int check_out_rows(const void* p, int64_t T, int64_t heads, int64_t tok, int64_t head, int64_t D) {
+  if (int rc = check_rows(p, heads, tok, head, D)) return rc;
+  const bool tokens_apart = T == 1 || tok >= (heads - 1) * head + D;
+  const bool heads_apart = heads == 1 || (T > 1 && head >= (T - 1) * tok + D);
+  if (heads == 1 ? T > 1 && tok < D : !tokens_apart && !(heads_apart && tok >= D)) return FP8_ERR_INVALID_ARG;
+  return FP8_OK;
+}
+
 int check_rope(int64_t R, int64_t D, const float* cos_sin, int64_t max_pos, const int64_t* pos) {
   if (R < 0 || R > D) return FP8_ERR_INVALID_ARG;
   if (R % 16 != 0) return FP8_ERR_SHAPE;
@@ -848,11 +857,11 @@ int fp8_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head, const void* k
   if (T == 0 || Hq + Hk == 0) return FP8_OK;
   if (Hq > 0) {
     if (int rc = check_rows(q, Hq, q_tok, q_head, D)) return rc;
-    if (int rc = check_rows(qo, Hq, qo_tok, qo_head, D)) return rc;
+    if (int rc = check_out_rows(qo, T, Hq, qo_tok, qo_head, D)) return rc;
   }
   if (Hk > 0) {
     if (int rc = check_rows(k, Hk, k_tok, k_head, D)) return rc;
-    if (int rc = check_rows(ko, Hk, ko_tok, ko_head, D)) return rc;
+    if (int rc = check_out_rows(ko, T, Hk, ko_tok, ko_head, D)) return rc;
   }
   if ((wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return FP8_ERR_ALIGNMENT;
   KvWriteArgs a{};
@@ -889,7 +898,7 @@ int fp8_qk_norm_rope_kv_write(const void* q, int64_t q_tok, int64_t q_head, cons
   if (int rc = check_rows(v, cache->heads, v_tok, v_head, D)) return rc;
   if (Hq > 0) {
     if (int rc = check_rows(q, Hq, q_tok, q_head, D)) return rc;
-    if (int rc = check_rows(qo, Hq, qo_tok, qo_head, D)) return rc;
+    if (int rc = check_out_rows(qo, T, Hq, qo_tok, qo_head, D)) return rc;
   }
   if (!aligned(slots, 8) || (wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return FP8_ERR_ALIGNMENT;
   KvWriteArgs a{};

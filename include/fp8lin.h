@@ -374,8 +374,8 @@ typedef struct {
  *   cos_sin    fp32 [max_pos][R]: R/2 cosines, then R/2 sines, of each position; 16-byte
  *              aligned.  R % 16 == 0, 0 <= R <= D; R == 0: no rotation, cos_sin and pos unused.
  *   pos        DEVICE int64 [T]; clamped into [0, max_pos).
- *   qo, ko     bf16 outputs with strides of their own; qo may be q and ko may be k (with the
- *              same strides), any other overlap is not allowed.
+ *   qo, ko     bf16 outputs with strides of their own, under which no two heads overlap; qo may
+ *              be q and ko may be k (with the same strides), any other overlap is not allowed.
  * Returns FP8_OK or an error status; T == 0 is a no-op.
  */
 int fp8_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head, const void* k, int64_t k_tok, int64_t k_head,

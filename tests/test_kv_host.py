@@ -70,6 +70,11 @@ def test_norm_rope_validation():
     assert norm_rope(k=(FAKE + 8, 256, 128)) == ALIGN
     assert norm_rope(q=(FAKE, 1028, 128)) == ALIGN
     assert norm_rope(q=(FAKE, 1024, 64)) == INVALID        # heads that overlap
+    assert norm_rope(qo=(FAKE, 0, 128)) == INVALID         # outputs whose tokens overlap
+    assert norm_rope(qo=(FAKE, 512, 128)) == INVALID
+    assert norm_rope(ko=(FAKE, 128, 128)) == INVALID
+    assert norm_rope(ko=(FAKE, 128, 384)) == INVALID       # heads first: 4 tokens of 128 channels
+    assert norm_rope(Hk=1, ko=(FAKE, 64, 128)) == INVALID
     assert norm_rope(wq=FAKE + 2) == ALIGN
     assert norm_rope(T=0, q=(None, 0, 0), k=(None, 0, 0), qo=(None, 0, 0), ko=(None, 0, 0), cs=None, pos=None) == OK
     assert norm_rope(Hq=0, Hk=0) == OK
@@ -93,6 +98,7 @@ def test_fused_validation():
     assert fused(R=136) == INVALID
     assert fused(R=24) == SHAPE
     assert fused(wk=FAKE + 8) == ALIGN
+    assert fused(qo=(FAKE, 896, 128)) == INVALID
     assert fused(T=2 ** 31) == SHAPE
     assert fused(T=0) == OK
     assert F.lib.fp8_kv_write(FAKE, 256, 128, FAKE, 256, 128, -4, FAKE, ctypes.byref(cache()), S) == INVALID

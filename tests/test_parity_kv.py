@@ -45,9 +45,10 @@ def norm_rope_ref(x, w, cs, pos, r, interleaved, eps=EPS):
 
 
 def check_bf16(got, y, size, what):
-    """One rounding to bf16 (2^-8) of an fp32 result off by at most 2^-20 of its terms: the sum
-    of squares takes 13 roundings (halved by the root), quotient, root and reciprocal 3, the
-    two products 2, the rotation 3, each 2^-24."""
+    """One rounding to bf16 (2^-8) of an fp32 result off by at most 2^-20 of its terms, in units of
+    2^-24: the sum of squares 10 (4 in a chain, 2 to join four chains, 4 over the lanes) and its
+    mean and eps 2, halved by the root; the reciprocal root's 2 ulp 4; two products 2; the
+    rotation 3; together 15."""
     err = (got.double() - y).abs()
     tol = 2.0 ** -8 * y.abs() + 2.0 ** -20 * size * (1 + 2.0 ** -8) + 2.0 ** -133
     assert (err <= tol).all(), f"{what}: worst {float((err / tol).max())} of the bound"
@@ -95,6 +96,19 @@ def test_norm_rope_in_place_on_a_projection(cuda_device):
     ref_q, ref_k = F.qk_norm_rope(q, k, pos, cs, w, w)
     F.fp8_qk_norm_rope(q, k, pos, cs, q, k, w, w)
     assert torch.equal(q, ref_q) and torch.equal(k, ref_k) and torch.equal(qkv[:, Hq + Hk:], before[:, Hq + Hk:])
+
+
+def test_broadcast_inputs_and_head_major_outputs(cuda_device):
+    """One token's q for all positions (a token stride of 0), outputs with heads first."""
+    T, H, D = 40, 3, 64
+    q = rand((1, H, D), 14).expand(T, H, D)
+    k = rand((T, H, D), 15)
+    pos, cs = torch.arange(T, device="cuda"), F.rope_table(64, D)
+    qo = torch.empty((H, T, D), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    ko = torch.empty_like(k)
+    F.fp8_qk_norm_rope(q, k, pos, cs, qo, ko)
+    check_bf16(qo, *norm_rope_ref(q, None, cs, pos, D, False), "q")
+    check_bf16(ko, *norm_rope_ref(k, None, cs, pos, D, False), "k")
 
 
 def test_far_and_outside_positions(cuda_device):
