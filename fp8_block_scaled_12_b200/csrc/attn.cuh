@@ -89,14 +89,15 @@ struct AttnCfg {
   // 105 us with 3), with fewer the loads show as soon as the clock drops (64 sequences of up to
   // 24000 tokens back to back for 80 ms: 252 us with 5, 258 us with 4, 280 us with 3).
   static constexpr int SLOTS = DCH == 2 ? 3 : 5;
-  static constexpr uint32_t Q_BYTES = 2 * GT * 128 * DCH;
+  static constexpr uint32_t Q_ROWS = GT == 4 ? 16 : 2 * GT;    // two pieces; at least the MMA's smallest N
+  static constexpr uint32_t Q_BYTES = Q_ROWS * 128 * DCH;
   static constexpr uint32_t P_ROW = 4 * GT;                  // bytes per token of the split weights
   static constexpr uint32_t P_BYTES = kAttnTile * P_ROW;
   static constexpr uint32_t OFF_Q = 2 * SLOTS * KV_BYTES;
   static constexpr uint32_t OFF_P = OFF_Q + 4 * Q_BYTES;     // queries: two buffers a warpgroup
   static constexpr uint32_t OFF_S = OFF_P + 2 * P_BYTES;     // scales: [warpgroup][kScaleRing][2][128] fp32
   static constexpr uint32_t OFF_STATE = OFF_S + 2 * kScaleRing * 1024;
-  static constexpr uint32_t S_COLS = 2 * GT, O_COLS = 4 * GT;
+  static constexpr uint32_t S_COLS = Q_ROWS, O_COLS = 4 * GT;
   static constexpr uint32_t TMEM_USED = 2 * (2 * S_COLS + DCH * O_COLS);     // two score buffers a warpgroup
   static constexpr uint32_t TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : 256;
 };
@@ -119,6 +120,7 @@ struct alignas(16) AttnState {            // arrays [2]: by warpgroup
   uint64_t qfull[2][2];    // [buffer]
   uint64_t sfull[2][2];    // [parity of its tile]
   uint64_t pfull[2], ofull[2];
+  uint64_t meet[2];        // the warpgroup's warps
   uint64_t drain[2];
   uint32_t boxes[2][kScaleRing];           // which boxes of the tile hold a valid page
   int seg[2][kScaleRing];                  // its segment of the worker's range
@@ -239,17 +241,6 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// Barrier of `threads` threads that also tells whether any of them has failed.
-__device__ __forceinline__ bool attn_barrier_or(int id, int threads, bool p) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(int(p)), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
 // Arrival on `bar` once this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -267,16 +258,38 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
 
 // Shared-memory descriptors.  K-major operands have rows of 128 bytes (the layout of
 // sw128_kmajor_desc); MN-major ones have rows along K that hold `row` bytes of the whole M or N,
-// written with the swizzle of that width.  Either way 8-row groups are row * 8 bytes apart
-// (stride offset) and the leading offset is unused.  The low word holds the address in units
-// of 16 bytes, so that steps are additions of constants to it.
-__device__ __forceinline__ uint32_t attn_desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+// written with the swizzle of that width (none for 16).  Either way 8-row groups are row * 8
+// bytes apart: the stride offset, or, without a swizzle, the leading one, which nothing else
+// uses here.  The low word holds the address in units of 16 bytes, so that steps are additions
+// of constants to it.
+__device__ __forceinline__ uint32_t attn_desc_lo(uint32_t addr, uint32_t row = 128) {
+  return (addr >> 4) | ((row == 16 ? (row * 8) >> 4 : 1u) << 16);
+}
 __device__ __forceinline__ uint64_t attn_desc(uint32_t lo, uint32_t row) {
-  const uint32_t layout = row == 128 ? 2u : row == 64 ? 4u : 6u;    // 128-, 64-, 32-byte swizzle
+  const uint32_t layout = row == 128 ? 2u : row == 64 ? 4u : row == 32 ? 6u : 0u;    // 128-, 64-, 32-byte swizzle
   const uint32_t hi = ((row * 8) >> 4) | (1u << 14) | (layout << 29);
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
   return d;
+}
+// Columns of tensor memory, N a thread.  The loads are for whole warps (.sync.aligned), so lanes
+// that a mask or a wait has parted meet first.
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  __syncwarp();
+  if constexpr (N == 8) {
+    tmem_ld8(taddr, r);
+  } else if constexpr (N == 16) {
+    tmem_ld16(taddr, r);
+  } else if constexpr (N == 32) {
+    tmem_ld32(taddr, r);
+  } else {
+    static_assert(N == 64, "columns a thread loads");
+    tmem_ld32(taddr, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+    tmem_ld32(taddr + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+  }
+  tmem_ld_wait();
+  tmem_regs_ready(r);
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -289,15 +302,17 @@ __device__ __forceinline__ constexpr uint32_t attn_idesc(int fmt, uint32_t n, bo
   return idesc_f8_e4m3_f32(128, n) | (uint32_t(fmt) << 7) | (mn ? (3u << 15) : 0u);
 }
 
-// fp32 pair -> two E4M3 codes and what they leave, times 16 (exact).
-__device__ __forceinline__ uint32_t split16(float& a, float& b) {
-  const uint32_t c = cvt2<kE4M3>(a, b);
+// fp32 pair -> two E4M3 codes, and what they leave, times 16 (exact), in its place.
+__device__ __forceinline__ uint32_t code2(uint64_t v) {
+  const float2 f = unpack2(v);
+  return cvt2<kE4M3>(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t split16(uint64_t& v) {
+  const uint32_t c = code2(v);
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(c)));
   const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-  const float2 o = unpack2(fma2(pack2(f.x, f.y), pack2(-16.0f, -16.0f), mul2(pack2(a, b), pack2(16.0f, 16.0f))));
-  a = o.x;
-  b = o.y;
+  v = fma2(pack2(f.x, f.y), pack2(-16.0f, -16.0f), mul2(v, pack2(16.0f, 16.0f)));
   return c;
 }
 
@@ -345,35 +360,38 @@ __device__ __forceinline__ void attn_scan(const AttnArgs& a, int lane, int wg, A
 
 // Queries of a segment -> two E4M3 pieces as K-major rows (hi: head g, lo: head GT + g) in
 // shared memory, and the factor that turns their products into base-2 exponents.  A thread
-// owns 8 or 16 channels of a head; loading and storing are apart, so that a tile's work hides the
-// loads' latency.
+// owns 4, 8 or 16 channels of a head; loading and storing are apart, so that a tile's work hides
+// the loads' latency.
 template <class C>
 struct AttnQuery {
-  static constexpr int UNIT = C::GT * C::DCH / 8 * 8;        // 128 threads share GT heads of 128 DCH channels
+  static constexpr int UNIT = C::GT * C::DCH;                // 128 threads share GT heads of 128 DCH channels
   static constexpr int UPH = 128 * C::DCH / UNIT;            // units per head
-  static_assert(C::GT * UPH == 128 && (UNIT == 8 || UNIT == 16), "one unit a thread");
-  uint4 v[UNIT / 8];
+  static_assert(C::GT * UPH == 128 && (UNIT == 4 || UNIT == 8 || UNIT == 16), "one unit a thread");
+  uint32_t x[UNIT / 2];
   __device__ __forceinline__ void load(const AttnArgs& a, const AttnWalk& w, int tid) {
     const int g = w.hc * C::GT + tid / UPH, ch = tid % UPH * UNIT;
 #pragma unroll
-    for (int i = 0; i < UNIT / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < UNIT / 2; ++i) x[i] = 0u;
     if (g < a.G && ch < a.D) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(w.b) * a.q_row + int64_t(w.c * a.G + g) * a.q_head +
-                                                      ch);
+      const uint16_t* p = a.q + int64_t(w.b) * a.q_row + int64_t(w.c * a.G + g) * a.q_head + ch;
+      if constexpr (UNIT == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        x[0] = v.x;
+        x[1] = v.y;
+      } else {
 #pragma unroll
-      for (int i = 0; i < UNIT / 8; ++i) v[i] = __ldg(p + i);
+        for (int i = 0; i < UNIT / 8; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          x[4 * i] = v.x;
+          x[4 * i + 1] = v.y;
+          x[4 * i + 2] = v.z;
+          x[4 * i + 3] = v.w;
+        }
+      }
     }
   }
   __device__ __forceinline__ void store(const AttnArgs& a, uint8_t* sq, float* cq, int tid) const {
     const int head = tid / UPH, ch = tid % UPH * UNIT;
-    uint32_t x[UNIT / 2];
-#pragma unroll
-    for (int i = 0; i < UNIT / 8; ++i) {
-      x[4 * i] = v[i].x;
-      x[4 * i + 1] = v[i].y;
-      x[4 * i + 2] = v[i].z;
-      x[4 * i + 3] = v[i].w;
-    }
     uint32_t mx = 0;                         // largest |q| as bf16 bits: NaN and Inf sort above all
 #pragma unroll
     for (int i = 0; i < UNIT / 2; ++i) mx = max(mx, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
@@ -385,47 +403,71 @@ struct AttnQuery {
     uint32_t hi[UNIT / 4], lo[UNIT / 4];
 #pragma unroll
     for (int i = 0; i < UNIT / 4; ++i) {
-      float p0 = bf16_lo(x[2 * i]) * up, p1 = bf16_hi(x[2 * i]) * up;
-      float p2 = bf16_lo(x[2 * i + 1]) * up, p3 = bf16_hi(x[2 * i + 1]) * up;
-      const uint32_t h0 = split16(p0, p1), h1 = split16(p2, p3);
+      uint64_t p0 = mul2(pack2(bf16_lo(x[2 * i]), bf16_hi(x[2 * i])), pack2(up, up));
+      uint64_t p1 = mul2(pack2(bf16_lo(x[2 * i + 1]), bf16_hi(x[2 * i + 1])), pack2(up, up));
+      const uint32_t h0 = split16(p0), h1 = split16(p1);
       hi[i] = bad ? 0x7F7F7F7Fu : h0 | (h1 << 16);
-      lo[i] = bad ? 0x7F7F7F7Fu : cvt2<kE4M3>(p0, p1) | (cvt2<kE4M3>(p2, p3) << 16);
+      lo[i] = bad ? 0x7F7F7F7Fu : code2(p0) | (code2(p1) << 16);
     }
-    // 128-byte swizzle of the row `head` (8 rows apart the pattern repeats, so row GT + head too)
-    uint8_t* at = sq + (ch >> 7) * (2 * C::GT * 128) + head * 128 + ((((ch >> 4) & 7) ^ (head & 7)) * 16) + (ch & 15);
-    if constexpr (UNIT == 8) {
+    // rows of 128 bytes with the 128-byte swizzle
+    uint8_t* chunk = sq + (ch >> 7) * (C::Q_ROWS * 128) + (ch & 15);
+    const int c16 = (ch >> 4) & 7, low = C::GT + head;
+    uint8_t* at = chunk + head * 128 + ((c16 ^ (head & 7)) * 16);
+    uint8_t* at_lo = chunk + low * 128 + ((c16 ^ (low & 7)) * 16);
+    if constexpr (UNIT == 4) {
+      *reinterpret_cast<uint32_t*>(at) = hi[0];
+      *reinterpret_cast<uint32_t*>(at_lo) = lo[0];
+    } else if constexpr (UNIT == 8) {
       *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(at + C::GT * 128) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(at_lo) = make_uint2(lo[0], lo[1]);
     } else {
       *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(at + C::GT * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(at_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     if (ch == 0) cq[head] = a.scale * 1.44269504088896340736f / up;
   }
 };
 
-// mbar_wait with the limit read once per kernel and a number of polls before the clock is
-// looked at: reading either costs more than most of this kernel's waits.
+// A wait by a whole warp, with mbar_wait's bounds.  Every branch in it is taken by all lanes or
+// none: a wait that lanes leave one by one, or that some of them skip (those of unmasked tokens,
+// say), can leave the warp in parts, and a part that reaches a barrier counts as the warp -- the
+// barrier then lets the other warps go without the rest, whose own wait there never ends.
+// The limit is read once per kernel and the clock only now and then: either costs more than
+// most of the waits.
 __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (limit_ns >= 1000) {
+  if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+  uint64_t since = 0;
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 1; i < FP8LIN_WAIT_ITERS && limit_ns >= 1000; ++i) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    if ((i & 31u) == 0u) {
+      if (__any_sync(~0u, *abort != 0)) return false;
+      const uint64_t now = __shfl_sync(~0u, globaltimer_ns(), 0);
+      if (since == 0) since = now;
+      if (now - since > limit_ns) break;
+    }
   }
-  return mbar_wait(bar, parity, abort, limit_ns);
+  if ((threadIdx.x & 31) == 0) {
+    *abort = 1;
+    atomicOr(&g_device_error, 1u);
+  }
+  __syncwarp();
+  return false;
 }
 
-// The same by a whole warp, all of whose lanes get the same answer.
-__device__ __forceinline__ bool attn_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  return __all_sync(~0u, attn_wait(bar, parity, abort, limit_ns));
+// Meeting of a warpgroup's four warps on an mbarrier (bounded, unlike a hardware barrier): what
+// they wrote to shared memory before it is visible after it.  False if a warp has given up.
+__device__ __forceinline__ bool attn_meet(uint32_t bar, int& turn, bool ok, volatile int* abort, uint64_t limit_ns) {
+  __syncwarp();
+  if (ok && (threadIdx.x & 31) == 0) mbar_arrive(bar);
+  return attn_wait(bar, uint32_t(turn++) & 1u, abort, limit_ns) && ok;
 }
 
 template <int FMT, class C>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     k_paged_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const AttnArgs a) {
-  constexpr int GT = C::GT, DCH = C::DCH, SLOTS = C::SLOTS;
+  constexpr int GT = C::GT, NP = GT / 2, DCH = C::DCH, SLOTS = C::SLOTS;
   using State = AttnState<GT, SLOTS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -449,6 +491,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       mbar_init(smem_u32(&ps->pfull[i]), 4);
       mbar_init(smem_u32(&ps->ofull[i]), 1);
+      mbar_init(smem_u32(&ps->meet[i]), 4);
       mbar_init(smem_u32(&ps->drain[i]), 1);
     }
     ps->abort = 0;
@@ -520,7 +563,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int64_t spage = __shfl_sync(~0u, pg, sbox);
           const int sr = __shfl_sync(~0u, rw, sbox) + srow;
           int s = u % SLOTS;
-          if (!attn_wait_warp(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
+          if (!attn_wait(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
           const int e = j % kScaleRing;
           if (lane == 0) {
             ps->boxes[g][e] = boxes;
@@ -544,7 +587,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           cp_async_arrive(smem_u32(&ps->scales[g][e]));
           ++u;
           s = u % SLOTS;
-          if (!attn_wait_warp(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
+          if (!attn_wait(smem_u32(&ps->empty[g][s]), ((u / SLOTS) & 1u) ^ 1u, abort, limit)) break;
           if (lane == 0) mbar_arrive_expect_tx(smem_u32(&ps->full[g][s]), C::KV_BYTES);
           __syncwarp();
           if (lane < nb) {
@@ -564,11 +607,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else {
       // ------------------------------------------------ MMAs
       // the whole warp walks, one elected lane issues: operands then stay in uniform registers
-      constexpr uint32_t id_s = attn_idesc(FMT, 2 * GT, false), id_o = attn_idesc(FMT, 4 * GT, true);
+      constexpr uint32_t id_s = attn_idesc(FMT, C::Q_ROWS, false), id_o = attn_idesc(FMT, 4 * GT, true);
       const int steps = (a.D + 31) / 32;
       const uint32_t rlo = attn_desc_lo(ring);
       const uint32_t qlo = attn_desc_lo(base + C::OFF_Q + 2 * g * C::Q_BYTES);
-      const uint32_t plo = attn_desc_lo(base + C::OFF_P + g * C::P_BYTES);
+      const uint32_t plo = attn_desc_lo(base + C::OFF_P + g * C::P_BYTES, C::P_ROW);
       const uint32_t tmem_s = tmem + 2 * g * C::S_COLS, tmem_o = tmem + 4 * C::S_COLS + g * (DCH * C::O_COLS);
       // Whichever product's operands are there goes first: in tile order, outputs whose weights
       // are ready would wait for a later tile's K and keep V's slot meanwhile.  Scores run up to two tiles ahead of the outputs:
@@ -593,7 +636,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int k = 0; k < 4 * DCH; ++k)
                   if (k < steps)
                     mma_f8(tmem_s + par * C::S_COLS, attn_desc(k0 + (k / 4) * (kAttnTile * 8) + (k % 4) * 2, 128),
-                           attn_desc(q0 + (k / 4) * (2 * GT * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
+                           attn_desc(q0 + (k / 4) * (C::Q_ROWS * 8) + (k % 4) * 2, 128), id_s, k > 0 ? 1u : 0u);
                 mma_commit(smem_u32(&ps->sfull[g][par]));
                 mma_commit(smem_u32(&ps->empty[g][s]));
               }
@@ -637,7 +680,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       for (int u = max(0, 2 * n - 2); ok && u < 2 * n; ++u)       // the last commits have arrived
-        ok = attn_wait_warp(smem_u32(&ps->empty[g][u % SLOTS]), (u / SLOTS) & 1u, abort, limit);
+        ok = attn_wait(smem_u32(&ps->empty[g][u % SLOTS]), (u / SLOTS) & 1u, abort, limit);
       if (*abort && lane == 0) {           // the MMAs already issued finish before tensor memory is freed
         mma_commit(smem_u32(&ps->drain[g]));
         mbar_drain(smem_u32(&ps->drain[g]), 0u);
@@ -668,21 +711,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       };
       qn.load(a, ahead, tok);
       stage(0);
-      bool ok = true;
-      attn_barrier_or(1 + wg, 128, false);         // the first segment's factors are visible
+      int turn = 0;
+      auto meet = [&](bool ok_) { return attn_meet(smem_u32(&ps->meet[wg]), turn, ok_, abort, limit); };
+      bool ok = meet(true);                        // the first segment's factors are visible
       int j = 0;                                   // this warpgroup's tile
       for (int seg = 0;; ++seg) {
         bool staging = ahead.next_segment(a);
         if (staging) qn.load(a, ahead, tok);
-        // fa, fb: the last tile's factors; lane i of every warp keeps the running maximum of head i % GT
-        float cq[GT], l[GT], o[DCH][GT], fa[GT], fb[GT], m = -INFINITY;
+        // pairs of heads; fa, fb: the last tile's factors.  Lane i of every warp keeps the running
+        // maximum of head i % GT.
+        uint64_t cq[NP], l[NP], o[DCH][NP], fa[NP], fb[NP];
+        float m = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < GT; ++g) {
-          cq[g] = ps->cq[wg][seg & 1][g];
-          l[g] = 0.0f;
-          fa[g] = fb[g] = 0.0f;
+        for (int i = 0; i < NP; ++i) {
+          cq[i] = pack2(ps->cq[wg][seg & 1][2 * i], ps->cq[wg][seg & 1][2 * i + 1]);
+          l[i] = fa[i] = fb[i] = 0u;
 #pragma unroll
-          for (int c = 0; c < DCH; ++c) o[c][g] = 0.0f;
+          for (int c = 0; c < DCH; ++c) o[c][i] = 0u;
         }
         // o = o * fa + (product of this warpgroup's tile j) * fb
         auto accumulate = [&](int j_) {
@@ -690,28 +735,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < DCH; ++c) {
-            uint32_t r[2][2 * GT];
-            if constexpr (GT == 8) {
-              tmem_ld16(tmem_o + c * C::O_COLS, r[0]);
-              tmem_ld16(tmem_o + c * C::O_COLS + 16, r[1]);
-            } else {
-              tmem_ld32(tmem_o + c * C::O_COLS, r[0]);
-              tmem_ld32(tmem_o + c * C::O_COLS + 32, r[1]);
-            }
-            tmem_ld_wait();
-            tmem_regs_ready(r[0]);
-            tmem_regs_ready(r[1]);
+            uint32_t r[4 * GT];
+            tmem_cols(tmem_o + c * C::O_COLS, r);
+            auto piece = [&](int k, int i) {
+              return pack2(__uint_as_float(r[k * GT + 2 * i]), __uint_as_float(r[k * GT + 2 * i + 1]));
+            };
+            const uint64_t k16 = pack2(0.0625f, 0.0625f), k256 = pack2(0.00390625f, 0.00390625f);
 #pragma unroll
-            for (int g = 0; g < GT; ++g) {
-              const float x = __uint_as_float(r[0][g]) + __uint_as_float(r[0][GT + g]) * 0.0625f;
-              const float y = __uint_as_float(r[1][g]) + __uint_as_float(r[1][GT + g]) * 0.0625f;
-              o[c][g] = fmaf(o[c][g], fa[g], fmaf(y, 0.00390625f, x) * fb[g]);
+            for (int i = 0; i < NP; ++i) {
+              const uint64_t x = fma2(piece(1, i), k16, piece(0, i)), y = fma2(piece(3, i), k16, piece(2, i));
+              o[c][i] = fma2(o[c][i], fa[i], mul2(fma2(y, k256, x), fb[i]));
             }
           }
         };
         const int t_first = w.t;
-        bool failed = false;
-        for (int t = t_first; t < w.t1; ++t, ++j) {
+        for (int t = t_first; ok && t < w.t1; ++t, ++j) {
           const int par = j & 1, e = j % kScaleRing;
           ok &= attn_wait(smem_u32(&ps->scales[wg][e]), (j / kScaleRing) & 1u, abort, limit);
           const float* sc = reinterpret_cast<const float*>(gbase + C::OFF_S + (wg * kScaleRing + e) * 1024);
@@ -724,16 +762,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float x[GT];
           {
             uint32_t r[2 * GT];
-            if constexpr (GT == 8) tmem_ld16(tmem_s + par * C::S_COLS, r);
-            else tmem_ld32(tmem_s + par * C::S_COLS, r);
-            tmem_ld_wait();
-            tmem_regs_ready(r);
+            tmem_cols(tmem_s + par * C::S_COLS, r);
             float wm[GT];
 #pragma unroll
-            for (int g = 0; g < GT; ++g) {
-              const float v = fmaf(__uint_as_float(r[GT + g]), 0.0625f, __uint_as_float(r[g])) * (cq[g] * sk);
-              x[g] = live ? v : -INFINITY;
-              wm[g] = warp_max(x[g]);
+            for (int i = 0; i < NP; ++i) {
+              const uint64_t hi = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+              const uint64_t lo = pack2(__uint_as_float(r[GT + 2 * i]), __uint_as_float(r[GT + 2 * i + 1]));
+              const float2 v = unpack2(mul2(fma2(lo, pack2(0.0625f, 0.0625f), hi), mul2(cq[i], pack2(sk, sk))));
+              x[2 * i] = live ? v.x : -INFINITY;
+              x[2 * i + 1] = live ? v.y : -INFINITY;
+              wm[2 * i] = warp_max(x[2 * i]);
+              wm[2 * i + 1] = warp_max(x[2 * i + 1]);
             }
             const float wv = warp_max(fabsf(sv));
             if (lane == 0) {
@@ -745,10 +784,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
           if (t > t_first) accumulate(j - 1);
-          if (attn_barrier_or(1 + wg, 128, !ok)) {
-            failed = true;
-            break;
-          }
+          ok = meet(ok);
+          if (!ok) break;
           const float4 vm = *reinterpret_cast<const float4*>(ps->redsv[wg][par]);
           // 2^E >= the largest sv (E >= -110: below that, values are tiny against any other)
           const int E = max(int(__float_as_uint(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))) >> 23) - 126, -110);
@@ -762,38 +799,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const float ref = mn == -INFINITY ? 0.0f : mn;        // nothing valid so far: every factor is 0
           const float la = ex2(m - ref), lb = ex2(tm - ref), lt = tm == -INFINITY ? 0.0f : tm;
           m = mn;
+          uint64_t v[NP];
 #pragma unroll
-          for (int g = 0; g < GT; ++g) {
-            const float p = ex2(x[g] - __shfl_sync(~0u, lt, g));
-            fa[g] = __shfl_sync(~0u, la, g);
-            const float be = __shfl_sync(~0u, lb, g);
-            l[g] = fmaf(l[g], fa[g], p * be);
-            fb[g] = be * down;
-            x[g] = p * rsv;
+          for (int i = 0; i < NP; ++i) {
+            const float p0 = ex2(x[2 * i] - __shfl_sync(~0u, lt, 2 * i));
+            const float p1 = ex2(x[2 * i + 1] - __shfl_sync(~0u, lt, 2 * i + 1));
+            const uint64_t p = pack2(p0, p1);
+            fa[i] = pack2(__shfl_sync(~0u, la, 2 * i), __shfl_sync(~0u, la, 2 * i + 1));
+            const uint64_t be = pack2(__shfl_sync(~0u, lb, 2 * i), __shfl_sync(~0u, lb, 2 * i + 1));
+            l[i] = fma2(l[i], fa[i], mul2(p, be));
+            fb[i] = mul2(be, pack2(down, down));
+            v[i] = mul2(p, pack2(rsv, rsv));
           }
           uint32_t pk[GT];                                      // [piece][heads], 4 codes a word
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
+          for (int k = 0; k < 3; ++k)
 #pragma unroll
-            for (int g = 0; g < GT; g += 4)
-              pk[i * (GT / 4) + g / 4] = split16(x[g], x[g + 1]) | (split16(x[g + 2], x[g + 3]) << 16);
+            for (int i = 0; i < NP; i += 2) pk[k * (GT / 4) + i / 2] = split16(v[i]) | (split16(v[i + 1]) << 16);
 #pragma unroll
-          for (int g = 0; g < GT; g += 4)
-            pk[3 * (GT / 4) + g / 4] = cvt2<kE4M3>(x[g], x[g + 1]) | (cvt2<kE4M3>(x[g + 2], x[g + 3]) << 16);
+          for (int i = 0; i < NP; i += 2) pk[3 * (GT / 4) + i / 2] = code2(v[i]) | (code2(v[i + 1]) << 16);
           uint8_t* pr = gbase + C::OFF_P + wg * C::P_BYTES + tok * C::P_ROW;
-          const int sw = GT == 8 ? (tok >> 2) & 1 : (tok >> 1) & 3;
+          const int sw = GT == 4 ? 0 : GT == 8 ? (tok >> 2) & 1 : (tok >> 1) & 3;
 #pragma unroll
           for (int i = 0; i < GT / 4; ++i)
             *reinterpret_cast<uint4*>(pr + ((i ^ sw) * 16)) =
                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-          if (!live && ((boxes >> (tok / a.BR)) & 1u)) {        // whatever the cache holds there times 0 is 0
+          const bool wipe = !live && ((boxes >> (tok / a.BR)) & 1u);
+          if (__any_sync(~0u, wipe)) {                          // whatever the cache holds there times 0 is 0
             const int u = 2 * j + 1, s = u % SLOTS;
             ok &= attn_wait(smem_u32(&ps->full[wg][s]), (u / SLOTS) & 1u, abort, limit);
-            uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(wg * SLOTS + s) * C::KV_BYTES + tok * 128);
+            if (wipe) {
+              uint4* vr = reinterpret_cast<uint4*>(gbase + uint32_t(wg * SLOTS + s) * C::KV_BYTES + tok * 128);
 #pragma unroll
-            for (int c = 0; c < DCH; ++c)
+              for (int c = 0; c < DCH; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) vr[c * (kAttnTile * 8) + (i ^ (tok & 7))] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 8; ++i) vr[c * (kAttnTile * 8) + (i ^ (tok & 7))] = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
           }
           fence_async_smem();
           tc_fence_before();
@@ -804,14 +846,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             staging = false;
           }
         }
-        if (failed) break;
+        if (!ok) break;
         accumulate(j - 1);
         // sums of p over the tokens
         {
-          const float s1 = warp_sums(l, lane);
+          float lg[GT];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float2 v = unpack2(l[i]);
+            lg[2 * i] = v.x;
+            lg[2 * i + 1] = v.y;
+          }
+          const float s1 = warp_sums(lg, lane);
           if ((lane & (32 / GT - 1)) == 0) ps->lsum[wg][quad][lane / (32 / GT)] = s1;
         }
-        if (attn_barrier_or(1 + wg, 128, !ok)) break;
+        ok = meet(ok);
+        if (!ok) break;
         const int g0 = w.hc * GT, heads = min(GT, a.G - g0);
         const bool whole = t_first == 0 && w.t1 == w.s.n;
         const int64_t head0 = (int64_t(w.b) * a.H + w.c) * a.G + g0;
@@ -835,7 +885,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __nv_bfloat16* po = reinterpret_cast<__nv_bfloat16*>(a.out) + head0 * a.D + ch * 128 + tok;
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-              const float v = o[ch][g] * __shfl_sync(~0u, inv, g);
+              const float2 og = unpack2(o[ch][g / 2]);
+              const float v = (g & 1 ? og.y : og.x) * __shfl_sync(~0u, inv, g);
               if (on && g < heads) *po = __float2bfloat16_rn(v);
               po += a.D;
             }
@@ -843,7 +894,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float* pw = a.ws_o + int64_t(slot) * GT * a.D + ch * 128 + tok;
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-              if (on && g < heads) *pw = o[ch][g];
+              const float2 og = unpack2(o[ch][g / 2]);
+              if (on && g < heads) *pw = g & 1 ? og.y : og.x;
               pw += a.D;
             }
           }

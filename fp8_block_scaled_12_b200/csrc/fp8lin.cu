@@ -397,9 +397,10 @@ bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t
   return r == CUDA_SUCCESS;
 }
 
-// Query heads of one kv head that a tile carries: 8, or 16 when a kv head has more (at most
-// 8 for heads of over 128 channels, whose tiles leave no shared memory for more).
-inline int attn_gt(int64_t G, int64_t D) { return G <= 8 || D > 128 ? 8 : 16; }
+// Query heads of one kv head that a tile carries: the least of 4, 8 and 16 that holds them, or
+// several chunks of the largest (8 for heads of over 128 channels, whose tiles leave no shared
+// memory for more).
+inline int attn_gt(int64_t G, int64_t D) { return G <= 4 ? 4 : G <= 8 || D > 128 ? 8 : 16; }
 inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1) / attn_gt(G, D); }
 
 // Workspace of the attention: two partial sums for each of two workers an SM, then one entry
@@ -432,9 +433,12 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
 
 template <int FMT>
 int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, int grid, cudaStream_t st) {
-  if (a.D > 128) return launch_attention<FMT, 8, 2>(mk, mv, a, grid, st);
-  return attn_gt(a.G, a.D) == 8 ? launch_attention<FMT, 8, 1>(mk, mv, a, grid, st)
-                                : launch_attention<FMT, 16, 1>(mk, mv, a, grid, st);
+  const int gt = attn_gt(a.G, a.D);
+  if (a.D > 128)
+    return gt == 4 ? launch_attention<FMT, 4, 2>(mk, mv, a, grid, st) : launch_attention<FMT, 8, 2>(mk, mv, a, grid, st);
+  return gt == 4   ? launch_attention<FMT, 4, 1>(mk, mv, a, grid, st)
+         : gt == 8 ? launch_attention<FMT, 8, 1>(mk, mv, a, grid, st)
+                   : launch_attention<FMT, 16, 1>(mk, mv, a, grid, st);
 }
 
 // Checks of a cache that every call shares.

@@ -209,6 +209,31 @@ def test_non_finite_values_that_count(cuda_device):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("H,G,D,P", [(8, 4, 128, 16), (2, 8, 128, 8), (2, 16, 64, 16), (4, 2, 192, 32)])
+def test_many_random_batches(cuda_device, H, G, D, P):
+    """Fifty batches of random lengths (partly masked tiles at the beginning, the middle and the end
+    of the workers' ranges): every wait ends, and a second call gives the same bits."""
+    g = torch.Generator().manual_seed(H * G + D)
+    pages = 8000
+    c = make_cache(pages, P, H, D)
+    for t in (c.k, c.v):
+        t.copy_(torch.randint(0, 124, t.shape, device="cuda").to(torch.uint8))
+    c.k_scale.uniform_(1e-4, 2e-3)
+    c.v_scale.uniform_(1e-3, 1e-2)
+    for i in range(50):
+        B = int(torch.randint(1, 70, (1,), generator=g))
+        lens = (torch.rand(B, generator=g) ** 3 * (pages * P // max(B, 16))).int()
+        width = max(1, int(-(-lens.max() // P)))
+        table = torch.randint(0, pages, (B, width), generator=g, dtype=torch.int32).cuda()
+        q = torch.randn((B, H * G, D), device="cuda").to(torch.bfloat16)
+        n = lens.cuda()
+        window = int(torch.randint(0, 3, (1,), generator=g)) * 333
+        out = F.paged_attention(q, c, table, n, window=window)
+        again = F.paged_attention(q, c, table, n, window=window)
+        assert F.fp8_device_error() == 0, (i, lens.tolist())
+        assert torch.isfinite(out).all() and torch.equal(out, again), (i, lens.tolist())
+
+
 def test_same_call_same_bits(cuda_device):
     c, table, q, n, out = case([5000, 1, 2999, 130, 900], 4, 8, 128, 16, seed=8)
     for _ in range(5):
