@@ -72,10 +72,11 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // LPH lanes own one head of one token, 16 channels each as two runs of 8 (a, b): for pairs
 // (i, R/2 + i) the two runs that rotate into each other, so that the rotation never leaves a
 // thread, else run j of each half of the head.  Loads and bf16 stores are 16 bytes a lane and
-// adjacent over the lanes.  A group of lanes keeps U heads (two, or one while one token a group is all
-// there is: the heads' latencies add up then) and goes from token to token: the norm's weights are loaded once, position, slot, cosines and sines serve all of its
-// heads, nothing is divided but the slot, and the channels of the next kWriteAhead tokens are
-// on their way through shared memory meanwhile.  A block works on one of q, k and v, so
+// adjacent over the lanes.  A group of lanes keeps U heads (two, or one while one token a group
+// is all there is: the heads' latencies add up then) and goes from token to token: the norm's
+// weights are loaded once, position, slot, cosines and sines serve all of its heads, nothing is
+// divided but the slot, and the channels of the next kWriteAhead tokens are on their way through
+// shared memory meanwhile.  A block works on one of q, k and v, so
 // pointers and strides stay in constant memory and what one of them does not need is not there.
 // Issue slots bound it next to memory, hence packed fp32 pairs throughout.  16384 tokens of
 // 32 + 8 + 8 heads of 128 in one pass: 66 us, 5.6 TB/s (with q, k and v mixed in a block 87 us,
@@ -279,9 +280,10 @@ __global__ void __launch_bounds__(256, 3) k_norm_rope_write(const __grid_constan
 // ------------------------------------------------------------------- read back
 // Row r of the outputs is token r - offsets[b] of the sequence b whose range holds r.  A block
 // takes a run of rows, its warps in turns, so that what it reads and writes at a time lies
-// together; a warp searches the offsets once and reads the table once a page.  Its steps are slices of 128 16-channel chunks of a row (k's heads, then v's), four chunks a
-// lane, and the next step's codes are loaded before this one's are converted.  Rows whose page
-// is not in the cache are zeros; rows outside every range are not written.
+// together; a warp searches the offsets once and reads the table once a page.  Its steps are
+// slices of 128 16-channel chunks of a row (k's heads, then v's), four chunks a lane, and the next
+// step's codes are loaded before this one's are converted.  Rows whose page is not in the cache
+// are zeros; rows outside every range are not written.
 // Bound by memory, two thirds of it the bf16 stores: 32 contexts of up to 4096 tokens, 8 heads
 // of 128: 74 us, 5.5 TB/s (92 us with two 16-byte stores in place of one of 32 bytes, 79 us with
 // runs of rows per warp).
