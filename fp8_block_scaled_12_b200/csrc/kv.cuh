@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(256, 2) k_kv_read(const KvReadArgs a) {
     else hi = mid;
   }
   int64_t next_b = __ldg(a.offsets + b + 1);
-  int tok = int(r - __ldg(a.offsets + b));
+  auto token = [&]() { return int(min(r - int64_t(__ldg(a.offsets + b)), int64_t(INT32_MAX))); };
+  int tok = token();
   int pi = tok / a.c.P, row = tok - pi * a.c.P;
   int64_t page;
   auto turn = [&]() {                         // the page of the current token
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(256, 2) k_kv_read(const KvReadArgs a) {
         if (r >= next_b) {                    // the sequence that has this row
           do next_b = __ldg(a.offsets + ++b + 1);
           while (r >= next_b);
-          tok = int(r - __ldg(a.offsets + b));
+          tok = token();
           pi = tok / a.c.P;
           row = tok - pi * a.c.P;
           turn();

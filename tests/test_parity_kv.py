@@ -263,3 +263,13 @@ def test_kv_read_beyond_the_table(cuda_device):
     off = torch.tensor([0, 12], dtype=torch.int32, device="cuda")
     ko, _ = F.kv_read(c, table, off, 12)
     assert (ko[:8] == 1).all() and (ko[8:] == 0).all()
+
+
+def test_kv_read_of_offsets_far_below_zero(cuda_device):
+    """The host cannot check device offsets: token numbers past 32 bits count as beyond the table."""
+    c = make_cache(4, 16, 2, 64)
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    off = torch.tensor([-2 ** 31, 12], dtype=torch.int32, device="cuda")
+    ko, vo = F.kv_read(c, table, off, 12)
+    assert F.fp8_device_error() == 0
+    assert (ko == 0).all() and (vo == 0).all()
