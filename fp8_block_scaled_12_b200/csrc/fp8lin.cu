@@ -947,7 +947,8 @@ int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_s
 }
 
 int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache) {
-  if (B < 0 || Hq <= 0 || check_cache(cache) != FP8_OK || Hq % cache->heads != 0) return 0;
+  if (B < 0 || B > INT32_MAX || Hq <= 0 || Hq > 65535) return 0;
+  if (check_cache(cache) != FP8_OK || Hq % cache->heads != 0) return 0;
   return AttnWs(B, cache->heads, Hq / cache->heads, cache->head_dim).total;
 }
 

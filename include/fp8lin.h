@@ -388,7 +388,8 @@ int fp8_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head, const void* k
  *   k, v       bf16 [T][heads][D], strides as above.
  *   slots      DEVICE int64 [T]: slot = page * page_size + row.  A slot outside
  *              [0, num_pages * page_size) (a padding row, say -1) is skipped.  The slots of
- *              one call must differ; which token a repeated slot holds is unspecified.
+ *              one call must differ; what a repeated slot holds is unspecified (codes of
+ *              one token, say, and the scale of another).
  * Codes and scales are those of fp8_act_quant with the head as its group.
  */
 int fp8_kv_write(const void* k, int64_t k_tok, int64_t k_head, const void* v, int64_t v_tok, int64_t v_head, int64_t T,
@@ -408,7 +409,7 @@ int fp8_qk_norm_rope_kv_write(const void* q, int64_t q_tok, int64_t q_head, cons
  * fp8_kv_read -- the first tokens of B sequences back as bf16 rows, bf16_rne(decode(code) * s)
  * (the context of a chunked prefill, say).
  *   table      DEVICE int32 [B][max_pages], row stride table_stride >= max_pages: page ids.
- *   offsets    DEVICE int32 [B + 1], non-decreasing: rows [offsets[b], offsets[b + 1]) of the
+ *   offsets    DEVICE int32 [B + 1], non-decreasing from >= 0: rows [offsets[b], offsets[b + 1]) of the
  *              outputs are tokens 0, 1, ... of sequence b.
  *   ko, vo     bf16 [rows][heads][D], 32-byte aligned.  Rows outside every range are not
  *              written; tokens beyond the table or of a page outside the cache are zeros.
@@ -432,7 +433,9 @@ int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_s
  *              16-byte aligned, no initial contents; calls that share it must be ordered on
  *              one stream (two captured graphs that share it must not run at once).
  * Scores, softmax and sums are fp32; the probabilities enter the second product with 17
- * significant bits.  The result does not depend on timing.
+ * significant bits.  The result does not depend on timing.  A token that counts and whose
+ * v_scale is infinite makes its row NaN.
+ * fp8_paged_attention_ws_bytes returns 0 for a cache or counts that the call would refuse.
  */
 int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache);
 

@@ -235,3 +235,8 @@ def test_c_client_and_structure_layout(tmp_path):
     s = _CacheStruct
     assert [int(x) for x in r.stdout.split()] == [ctypes.sizeof(s), s.v_scale.offset, s.num_pages.offset,
                                                   s.token_stride.offset, s.scale_fmt.offset]
+
+
+@pytest.mark.parametrize("B,Hq", [(2 ** 31, 8), (2 ** 62, 8), (1, 65536), (-1, 8), (1, 0), (1, 3)])
+def test_no_workspace_for_counts_that_the_call_refuses(B, Hq):
+    assert F.lib.fp8_paged_attention_ws_bytes(B, Hq, ctypes.byref(cache())) == 0
