@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ps->tmem_base;                 // scores of both warpgroups, then outputs
+  int u = 0;                                           // loaders: half tiles (K, then V) given a slot
   // (8 heads fit the registers of an even split)
   if (warp < 4) {
     if constexpr (GT > 8) setmaxnreg_dec<kAttnLoadRegs>();
@@ -526,7 +527,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // ------------------------------------------------ pages and scales -> shared memory
       // a lane owns a box of the tile and the scales of four tokens (rows of a box come in
       // multiples of eight)
-      int u = 0;                             // half tiles (K, then V) given a slot
       if (n > 0) {
         AttnWalk w;
         w.start(a, ps->range[g].b, ps->range[g].off, n);
@@ -607,10 +607,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           ++u;
         }
       }
-      if (*abort) {                      // every load already issued lands before the CTA exits
-        for (int i = max(0, u - SLOTS); i < u; ++i) mbar_drain(smem_u32(&ps->full[g][i % SLOTS]), (i / SLOTS) & 1u);
-        cp_async_wait_all();
-      }
       if (warp == 0) pdl_trigger();
     } else {
       // ------------------------------------------------ MMAs
@@ -690,10 +686,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       for (int u = max(0, 2 * n - 2); ok && u < 2 * n; ++u)       // the last commits have arrived
         ok = attn_wait(smem_u32(&ps->empty[g][u % SLOTS]), (u / SLOTS) & 1u, abort, limit);
-      if (*abort && lane == 0) {           // the MMAs already issued finish before tensor memory is freed
-        mma_commit(smem_u32(&ps->drain[g]));
-        mbar_drain(smem_u32(&ps->drain[g]), 0u);
-      }
     }
   } else {
     if constexpr (GT > 8) setmaxnreg_inc<kAttnSoftmaxRegs>();
@@ -798,7 +790,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const float4 vm = *reinterpret_cast<const float4*>(ps->redsv[wg][par]);
           // 2^E >= the largest sv (E >= -110: below that, values are tiny against any other)
           const int E = max(int(__float_as_uint(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))) >> 23) - 126, -110);
-          const float rsv = sv * __uint_as_float(uint32_t(8 - E + 127) << 23);
+          // (an infinite scale makes its token NaN: E4M3 would saturate without a trace)
+          const float rsv = fabsf(sv) == INFINITY ? NAN : sv * __uint_as_float(uint32_t(8 - E + 127) << 23);
           const float down = __uint_as_float(uint32_t(E - 8 + 127) << 23);
           // lane i: the factors of head i % GT
           const int hg = lane & (GT - 1);
@@ -921,9 +914,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // After a wait that ran out, loads and MMAs may still be under way, also those of warps that
+  // had come to their end by then: all land before shared and tensor memory are given back.
+  // (Nobody sets the flag any more, so all threads see the same.)
+  if (*abort) {
+    const int g = warp & 1;
+    if (warp < 2) {
+      for (int i = max(0, u - SLOTS); i < u; ++i)
+        mbar_drain(smem_u32(&ps->full[g][i % SLOTS]), (i / SLOTS) & 1u);
+      cp_async_wait_all();
+    } else if (warp < 4) {
+      if (elect_one()) {
+        mma_commit(smem_u32(&ps->drain[g]));
+        mbar_drain(smem_u32(&ps->drain[g]), 0u);
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 

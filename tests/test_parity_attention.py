@@ -209,6 +209,26 @@ def test_non_finite_values_that_count(cuda_device):
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_non_finite_value_scales_that_count(cuda_device, bad):
+    """A token whose v scale is not finite makes the heads that read it NaN in every channel,
+    also those where its code is zero, and no other head."""
+    lens, P, H, G, D = [300], 16, 2, 4, 64
+    c = make_cache(20, P, H, D)
+    table = make_table(lens, P, 20, 7)
+    fill_cache(c, table, lens, 7)
+    q = torch.randn((1, H * G, D), device="cuda").to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    clean = F.paged_attention(q, c, table, n)
+    page = table[0, 9].item()
+    c.v[page, 1, 3, :8] = 0
+    c.v_scale[page, 1, 3] = bad
+    out = F.paged_attention(q, c, table, n)
+    assert F.fp8_device_error() == 0
+    assert torch.isnan(out[0, G:]).all()
+    assert torch.equal(out[0, :G], clean[0, :G])
+
+
 @pytest.mark.parametrize("H,G,D,P", [(8, 4, 128, 16), (2, 8, 128, 8), (2, 16, 64, 16), (4, 2, 192, 32)])
 def test_many_random_batches(cuda_device, H, G, D, P):
     """Fifty batches of random lengths (partly masked tiles at the beginning, the middle and the end
