@@ -162,3 +162,39 @@ def test_workspace_and_output_are_not_read(cuda_device):
         out = torch.full_like(ref, float("nan"))
         F.fp8_paged_attention(q, blk.cache, blk.table, blk.n, out, ws)
         assert torch.equal(out, ref)
+
+
+def test_pages_beyond_32_bit_offsets(cuda_device):
+    """Write, read and attention on the last pages of a cache of 4.9 GB of k and as much of v, and
+    on its first: byte offsets and elements pass 32 bits between them."""
+    pages, P, H, G, D = 75000, 64, 8, 4, 128
+    assert pages * P * H * D > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for layout in ("HND", "NHD"):
+        c = F.KVCache(pages, P, H, D, layout=layout)
+        lens = [300, 77]
+        table = torch.tensor([[pages - 1, pages - 3, 0, pages - 7, 2], [pages - 2, 1, 5, 5, 5]], dtype=torch.int32,
+                             device="cuda")
+        kv, slots = [], []
+        for b, n in enumerate(lens):
+            t = torch.arange(n, device="cuda")
+            slots.append(table[b].long()[t // P] * P + t % P)
+        slots = torch.cat(slots)
+        k, v = (torch.randn((sum(lens), H, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        F.kv_write(k, v, slots, c)
+        off = torch.tensor([0, 300, 377], dtype=torch.int32, device="cuda")
+        kb, vb = F.kv_read(c, table, off, sum(lens))
+        page, row = slots // P, slots % P
+        k64, v64 = (x[page, :, row].view(torch.float8_e4m3fn).double() * s[page, :, row].double()[..., None]
+                    for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+        for got, want, src in ((kb, k64, k), (vb, v64, v)):
+            assert torch.equal(got, want.to(torch.float32).to(torch.bfloat16))
+            # a code is off by half a step of its value, 2^-4, or of the smallest step, 2^-10 of 448
+            amax = src.double().abs().amax(-1, keepdim=True)
+            assert ((want - src.double()).abs() <= src.double().abs() * 2 ** -4 + amax * 2 ** -10 / 448).all()
+        q = torch.randn((2, H * G, D), generator=g, device="cuda").to(torch.bfloat16)
+        out = F.paged_attention(q, c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        assert F.fp8_device_error() == 0
+        ref, _, tol, _ = attention_ref(q, [(k64[:300], v64[:300]), (k64[300:], v64[300:])], None, 0)
+        check_attention(out, ref, tol, "out")
+        del c
