@@ -406,8 +406,8 @@ bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t
 inline int attn_gt(int64_t G, int64_t D) { return G <= 4 ? 4 : G <= 8 || D > 128 ? 8 : 16; }
 inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1) / attn_gt(G, D); }
 
-// Workspace of the attention: two partial sums for each of two workers an SM, then one entry
-// per row.
+// Workspace of the attention: two partial sums for each of two workers an SM, then the entries of
+// the rows to join (one a row, or, of more rows than workers, one a worker).
 struct AttnWs {
   int64_t slots, o, ml, row, total;
   AttnWs(int64_t B, int64_t H, int64_t G, int64_t D) {
@@ -430,8 +430,8 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
   if (const int st_ = kernel_setup<(GT > 8)>(ready, kern, smem)) return st_;
   if (launch(kern, unsigned(grid), kAttnThreads, smem, st, mk, mv, a) != cudaSuccess) return FP8_ERR_CUDA;
   const int heads = a.G < GT ? a.G : GT;
-  return cuda_status(launch(k_attn_join<GT>, dim3(unsigned(int64_t(a.B) * a.H * a.HC), unsigned(heads)),
-                            kJoinThreads, 0, st, a));
+  const unsigned rows = unsigned(a.by_row ? a.B * a.H * a.HC : 2 * grid);
+  return cuda_status(launch(k_attn_join<GT>, dim3(rows, unsigned(heads)), kJoinThreads, 0, st, a));
 }
 
 template <int FMT>
@@ -993,12 +993,13 @@ int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B,
   a.lse = lse;
   a.ws_o = reinterpret_cast<float*>(w + ws.o);
   a.ws_ml = reinterpret_cast<float*>(w + ws.ml);
-  a.ws_row = reinterpret_cast<int2*>(w + ws.row);
+  a.ws_join = reinterpret_cast<int2*>(w + ws.row);
   a.q_row = q_row, a.q_head = q_head, a.table_stride = table_stride;
   a.window = window, a.cap = max_pages * P, a.pages = cache->num_pages, a.scale = scale;
   a.B = int(B), a.H = int(H), a.G = int(G), a.HC = int(HC), a.D = int(D), a.P = int(P), a.BR = int(br);
   a.slots = int(ws.slots);
   const int grid = int(tiles < num_sms() ? tiles : num_sms());
+  a.by_row = B * H * HC <= 2 * grid;               // else 2 * grid entries, which fit where the rows' would
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cache->fmt == FP8_E4M3 ? launch_attention<kE4M3>(mk, mv, a, grid, st)
                                 : launch_attention<kE5M2>(mk, mv, a, grid, st);
