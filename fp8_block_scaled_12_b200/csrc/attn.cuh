@@ -35,9 +35,9 @@
 //
 // Measured (32 query and 8 kv heads of 128, e4m3, ragged lengths; bytes of the cache over time,
 // both kernels, replayed from a graph): 64 sequences of up to 24000 tokens in pages of 32,
-// 1.63 GB, 249 us, 6.5 TB/s, the speed of a copy; 32 of up to 8192 in pages of 16, 286 MB, 54 us,
+// 1.63 GB, 247 us, 6.6 TB/s, the speed of a copy; 32 of up to 8192 in pages of 16, 286 MB, 54 us,
 // 5.2 TB/s (~4 us until the first tiles are there, ~5 us for the join and its launch); 131071 +
-// 50070 tokens of 64 / 8 heads, token-major, 383 MB, 78 us, 4.9 TB/s (rows of 128 bytes 1 KB
+// 50070 tokens of 64 / 8 heads, token-major, 383 MB, 77 us, 4.9 TB/s (rows of 128 bytes 1 KB
 // apart; head-major pages 67 us).  With the two warpgroups on alternate tiles of one range and
 // one ring the first two took 318 and 83 us, with one warpgroup 396 and 113.
 //
