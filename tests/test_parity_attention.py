@@ -258,3 +258,22 @@ def test_same_call_same_bits(cuda_device):
     c, table, q, n, out = case([5000, 1, 2999, 130, 900], 4, 8, 128, 16, seed=8)
     for _ in range(5):
         assert torch.equal(F.paged_attention(q, c, table, n), out)
+
+
+@pytest.mark.parametrize("B,H,L", [(80, 8, 700), (300, 2, 1), (600, 1, 300), (37, 8, 2000)])
+def test_rows_around_the_number_of_workers_any_workspace(cuda_device, B, H, L):
+    """More rows than workers and fewer, cut and whole: what the workspace holds before does not
+    matter, not even what looks like an entry of an earlier call."""
+    G, D, P = 4, 64, 16
+    lens = [(i * 7919) % (L + 1) for i in range(B)]
+    c, table, q, n, out = case(lens, H, G, D, P, seed=9)
+    ws = torch.empty(F.paged_attention_ws_bytes(B, H * G, c), dtype=torch.uint8, device="cuda")
+    for fill in (0, 1, 0x7F, 0xFF):
+        ws.fill_(fill)
+        again = torch.full_like(out, math.nan)
+        F.fp8_paged_attention(q, c, table, n, again, ws)
+        assert torch.equal(again, out)
+        F.fp8_paged_attention(q, c, table, torch.flip(n, [0]).contiguous(), again, ws)     # other cuts, then the same
+        F.fp8_paged_attention(q, c, table, n, again, ws)
+        assert torch.equal(again, out)
+    assert F.fp8_device_error() == 0
