@@ -289,7 +289,12 @@ __device__ __forceinline__ void ffma2(uint64_t& acc, uint32_t p_lo, uint32_t p_h
       : "r"(p_lo), "r"(p_hi), "l"(s2));
 }
 
-// Two independent, correctly rounded fp32 products / FMAs in one packed instruction.
+// Two independent, correctly rounded fp32 sums / products / FMAs in one packed instruction.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));

@@ -432,9 +432,13 @@ int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_s
  *   workspace  DEVICE scratch of at least fp8_paged_attention_ws_bytes(B, Hq, cache) bytes,
  *              16-byte aligned, no initial contents; calls that share it must be ordered on
  *              one stream (two captured graphs that share it must not run at once).
- * Scores, softmax and sums are fp32; the probabilities enter the second product with 17
- * significant bits.  The result does not depend on timing.  A token that counts and whose
- * v_scale is infinite makes its row NaN.
+ * Scores, softmax and sums are fp32.  q enters the first product exactly down to 2^-14 of its
+ * head's largest element, and off by at most 2^-21 of that below.  Probability times v_scale
+ * enters the second with 17 significant bits, or, where it is small against others, off by at
+ * most 2^-29 of the head's largest among the tokens [128 i, 128 i + 128) it stands with (2^-21
+ * for v scales below 2^-118; scales among them below 2^-90 of the largest count as that for
+ * this bound).  The result does not depend on timing.  A token that counts and whose v_scale
+ * is infinite makes its row NaN.
  * fp8_paged_attention_ws_bytes returns 0 for a cache or counts that the call would refuse.
  */
 int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache);
