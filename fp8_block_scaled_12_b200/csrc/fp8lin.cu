@@ -444,6 +444,15 @@ int launch_attention(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
                    : launch_attention<FMT, 16, 1>(mk, mv, a, grid, st);
 }
 
+// Sequences and query heads that the attention takes: the kernel counts rows, and the list of
+// their tiles (at least one each, and what a row costs besides), in 32 bits.
+int check_attn_counts(int64_t B, int64_t Hq, const fp8_kv_cache* c) {
+  if (B < 0 || Hq <= 0) return FP8_ERR_INVALID_ARG;
+  if (B > INT32_MAX || Hq > 65535 || Hq % c->heads != 0) return FP8_ERR_SHAPE;
+  const int64_t rows = B * c->heads * attn_chunks(Hq / c->heads, c->head_dim);
+  return rows > INT32_MAX / (1 + kAttnRowCost) ? FP8_ERR_SHAPE : FP8_OK;
+}
+
 // Checks of a cache that every call shares.
 int check_cache(const fp8_kv_cache* c) {
   if (!c) return FP8_ERR_INVALID_ARG;
@@ -947,8 +956,7 @@ int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_s
 }
 
 int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache) {
-  if (B < 0 || B > INT32_MAX || Hq <= 0 || Hq > 65535) return 0;
-  if (check_cache(cache) != FP8_OK || Hq % cache->heads != 0) return 0;
+  if (check_cache(cache) != FP8_OK || check_attn_counts(B, Hq, cache) != FP8_OK) return 0;
   return AttnWs(B, cache->heads, Hq / cache->heads, cache->head_dim).total;
 }
 
@@ -959,12 +967,10 @@ int fp8_paged_attention(const void* q, int64_t q_row, int64_t q_head, int64_t B,
   if (B < 0 || Hq <= 0 || max_pages < 0 || table_stride < max_pages || window < 0) return FP8_ERR_INVALID_ARG;
   if (!(scale > -3.0e38f && scale < 3.0e38f)) return FP8_ERR_INVALID_ARG;
   if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_attn_counts(B, Hq, cache)) return rc;
   const int64_t H = cache->heads, D = cache->head_dim, P = cache->page_size;
-  if (Hq % H != 0) return FP8_ERR_SHAPE;
   const int64_t G = Hq / H, HC = attn_chunks(G, D);
-  if (B > INT32_MAX || Hq > 65535 || B * H * HC > INT32_MAX) return FP8_ERR_SHAPE;
   if (max_pages > INT32_MAX / P || max_pages * P > INT32_MAX - 2 * kAttnTile) return FP8_ERR_SHAPE;
-  // (the list of tiles counts in 32 bits)
   const int64_t tiles = B * H * HC * ((max_pages * P + kAttnTile - 1) / kAttnTile + 1 + kAttnRowCost);
   if (tiles > INT32_MAX) return FP8_ERR_SHAPE;
   if (B == 0) return FP8_OK;

@@ -240,3 +240,16 @@ def test_c_client_and_structure_layout(tmp_path):
 @pytest.mark.parametrize("B,Hq", [(2 ** 31, 8), (2 ** 62, 8), (1, 65536), (-1, 8), (1, 0), (1, 3)])
 def test_no_workspace_for_counts_that_the_call_refuses(B, Hq):
     assert F.lib.fp8_paged_attention_ws_bytes(B, Hq, ctypes.byref(cache())) == 0
+
+
+@pytest.mark.parametrize("B", [1, 2 ** 20, 2 ** 28, (2 ** 31 - 1) // 6, (2 ** 31 - 1) // 6 + 1, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("Hq", [2, 8, 34, 65534, 65536])
+@pytest.mark.parametrize("D", [128, 256])
+def test_workspace_and_call_refuse_the_same_counts(B, Hq, D):
+    """The narrowest table there is, so the counts alone decide; the call stops at its missing outputs."""
+    c = cache(head_dim=D, token_stride=D, head_stride=16 * D, page_stride=32 * D)
+    n = F.lib.fp8_paged_attention_ws_bytes(B, Hq, ctypes.byref(c))
+    status = F.lib.fp8_paged_attention(FAKE, Hq * D, D, B, Hq, ctypes.byref(c), None, 0, 0, None, 0.1, 0, None, None,
+                                       None, 1 << 62, S)
+    assert status in (INVALID, SHAPE)
+    assert (n > 0) == (status == INVALID)
