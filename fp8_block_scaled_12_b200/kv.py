@@ -60,7 +60,11 @@ class KVCache:
     """Device memory of a paged cache: codes `k`, `v` (uint8, logical shape [num_pages, heads,
     page_size, head_dim]) and scales `k_scale`, `v_scale` (fp32 [num_pages, heads, page_size]).
     `layout`: "HND" keeps a head's tokens of a page together, "NHD" a token's heads.  The
-    memory is not initialised: readers use only what was written."""
+    memory is not initialised: readers use only what was written.  The tensors and formats may
+    be replaced by others that fit (all checks of `wrap` again; sizes follow from them); the
+    memory of those that are there has to stay in its place."""
+
+    _PARTS = ("k", "v", "k_scale", "v_scale", "fmt", "scale_fmt")
 
     def __init__(self, num_pages: int, page_size: int, heads: int, head_dim: int, fmt: int = E4M3,
                  scale_fmt: int = SCALE_FP32, layout: str = "HND", device="cuda"):
@@ -102,13 +106,20 @@ class KVCache:
                 raise ValueError(f"{name} must be contiguous")
         if any(t.device != k.device for t in (v, k_scale, v_scale)):
             raise ValueError("the cache's tensors live on different devices")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.fmt, self.scale_fmt = fmt, scale_fmt
-        self.num_pages, self.heads, self.page_size, self.head_dim = pages, heads, page, dim
-        self.device, self.index = k.device, k.get_device()
-        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page,
-                                    heads, dim, k.stride(0), k.stride(1), k.stride(2), fmt, scale_fmt)
-        self._ref = ctypes.addressof(self._struct)
+        # a structure of its own each time: calls and copies of this object may hold the last one
+        struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page, heads,
+                              dim, k.stride(0), k.stride(1), k.stride(2), fmt, scale_fmt)
+        vars(self).update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, fmt=fmt, scale_fmt=scale_fmt, num_pages=pages,
+                          heads=heads, page_size=page, head_dim=dim, device=k.device, index=k.get_device(),
+                          _ref=ctypes.byref(struct))
+
+    def __setattr__(self, name, value):
+        if name in self._PARTS:
+            self._set(**{n: value if n == name else getattr(self, n) for n in self._PARTS})
+        elif name in vars(self):
+            raise AttributeError(f"{name} of a cache follows from its tensors")
+        else:
+            super().__setattr__(name, value)
 
 
 def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
