@@ -4,10 +4,11 @@
 // of the sequence (its length, its window and its valid pages decide which):
 //   s_t = scale * sk_t * sum_d q_d dec(k_t[d])            p_t = exp(s_t - max s)
 //   out = (sum_t p_t sv_t dec(v_t)) / sum_t p_t
-// What bounds it: the cache is read once, 2 D + 8 bytes a token and kv head, against 4 D G
-// flops, so HBM does up to about a hundred heads per kv head.  The kernel is built so that
-// no code byte is ever converted: both products run on the FP8 tensor cores straight from
-// the tiles TMA has put into shared memory.
+// What bounds it: the cache is read once per chunk of up to 16 query heads of a kv head (8 with
+// more than 128 channels), 2 D + 8 bytes a token and kv head, against 4 D G flops, so HBM does up
+// to about a hundred heads per kv head.  The kernel is built so that no code byte is ever
+// converted: both products run on the FP8 tensor cores straight from the tiles TMA has put into
+// shared memory.
 //   scores   S^T[128 tokens x heads] = K-tile (A, 128 x D) . q^T.  A bf16 q (8 significant
 //            bits) is split into two E4M3 pieces q = (hi + lo / 16) 2^-e, 4 bits each with
 //            e from the head's largest |q|: exact for every element above 2^-14 of the

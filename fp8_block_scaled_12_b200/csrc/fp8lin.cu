@@ -308,10 +308,12 @@ int launch_tensor_quant(const uint16_t* x, int64_t n, uint8_t* q, float* s, cuda
 }
 
 // --------------------------------------------- paged key-value cache launches
-// The grid is shared out between q, k and v by their heads and what one costs (measured for
-// 16384 tokens of 32 + 8 + 8 heads of 128: 66 us with these shares, 82 us with equal ones,
-// 69 to 71 us with 8 for a turned head or 5 for a plain one); each gets blocks enough for all
-// of its heads of one token.
+// The grid is shared out between q, k and v by their heads and what one costs; each gets blocks
+// enough for all of its heads of one token.  The costs are those of fp32 scales.  32 + 8 + 8 heads,
+// 16384 tokens (8192 of 256 channels), these shares | equal ones: heads of 64 36.8 | 45.0 us, of
+// 128 66.5 | 83.2, of 256 64.4 | 82.7, of 128 with interleaved pairs 68.5 | 80.2; 8 for a turned
+// head or 5 for a plain one: 69 us at 128.  ue8m0 scales need no division, and equal shares would
+// be better there: 128 71.9 | 70.9 us, 256 73.3 | 68.8, 128 with interleaved pairs 74.7 | 69.9.
 constexpr int kCostBf16 = 4, kCostTurned = 7, kCostPlain = 4;
 
 template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
@@ -339,8 +341,13 @@ int launch_norm_rope_write(KvWriteArgs a, cudaStream_t st) {
   return cuda_status(launch(kern, unsigned(blocks), 256, 0, st, a));
 }
 
-// Heads per group of lanes: one while every group has a single token (64 tokens of 32 + 8 + 8
-// heads: 2.2 us against 3.1 us with two), two beyond (16384 tokens: 66 us against 91 us with one).
+// Heads per group of lanes: one while every group has a single token, two beyond.  32 + 8 + 8
+// heads, fp32 scales, one | two: of 128, 64 tokens 2.4 | 3.0 us, 200 3.0 | 3.1, 296 (the last with
+// one) 3.6 | 3.4, 400 3.8 | 4.1, 1000 6.6 | 6.6, 4000 20.2 | 19.3, 16384 72.0 | 66.6; of 64, 600
+// tokens 3.6 | 4.0, 2400 7.4 | 7.8, 16384 37.7 | 36.7; of 256, 148 tokens 3.7 | 3.5, 400 5.9 | 5.5,
+// 8192 72.4 | 64.4.  So two pay from some thousand tokens on, and near the switch neither side
+// is more than a tenth ahead.  Interleaved pairs with ue8m0 scales would stay ahead with one
+// (16384 tokens of 128: 69.5 | 74.7).
 template <int LPH, int ROPE, int FMT, int SF, bool CACHE>
 int launch_norm_rope_write(const KvWriteArgs& a, cudaStream_t st) {
   int64_t heads = 0;
@@ -399,10 +406,12 @@ bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t
 
 // Query heads of one kv head that a tile carries: the least of 4, 8 and 16 that holds them, or
 // several chunks of the largest (8 for heads of over 128 channels, whose tiles leave no shared
-// memory for more).  The softmax's issue slots decide: 64 ragged sequences of up to 8000 tokens
-// with 2 heads of 64 channels a kv head take 68 us with tiles of 4 and 83 us with tiles of 8
-// (512 of up to 1000 tokens with 4 of 128: 127 and 138 us); with 16 heads of 128 channels 121 us
-// with tiles of 16 and 177 us with two of 8.
+// memory for more).  Up to one chunk the softmax's issue slots decide: 64 ragged sequences of up to
+// 8000 tokens with 2 heads of 64 channels a kv head take 68 us with tiles of 4 and 83 us with
+// tiles of 8 (512 of up to 1000 tokens with 4 of 128: 127 and 138 us).  Every chunk is a row of
+// its own and loads its keys and values for itself, so the cache crosses the memory system once
+// per chunk: with 16 heads of 128 channels 121 us with tiles of 16 and 177 us with two of 8; 4 kv
+// heads of 128 with 32 heads each 124 us, with 16 each 68 us.
 inline int attn_gt(int64_t G, int64_t D) { return G <= 4 ? 4 : G <= 8 || D > 128 ? 8 : 16; }
 inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1) / attn_gt(G, D); }
 

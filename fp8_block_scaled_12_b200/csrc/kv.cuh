@@ -81,7 +81,9 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // Issue slots bound it next to memory, hence packed fp32 pairs throughout.  16384 tokens of
 // 32 + 8 + 8 heads of 128 in one pass: 66 us, 5.6 TB/s (with q, k and v mixed in a block 87 us,
 // one head a group 93 us, 8 channels a lane, scalar arithmetic and no loads ahead 133 us); the
-// same k and v alone: 21 us; norm and rotation of 4096 tokens of 32 + 8 heads: 16.3 us.
+// same k and v alone: 21 us (19 us with ue8m0 scales, which need no division); norm and rotation
+// of 4096 tokens of 32 + 8 heads: 16.3 us.  Three blocks an SM leave 80 registers: 36 of the 48
+// variants that write the cache and rotate spill 4 to 12 bytes a thread, the one measured 12.
 constexpr int kWriteAhead = 2;
 
 template <int LPH, int U, int ROPE, int FMT, int SF, bool CACHE>
