@@ -15,18 +15,16 @@
 //            largest and off by at most 2^-21 of the largest below that.  The pieces are
 //            2 x heads columns of B; tensor memory then holds one token per lane, so the
 //            token's scale is one register.
-//   softmax  per tile: with 2^e_t > sv_t, the maximum Y of s_t + e_t over the 128 tokens (in
-//            powers of two; one redux per warp and head, one exchange through shared memory),
-//            p = 2^(s - Y), and w = 2^8 p sv, whose largest then lies in [2^7, 2^8) for every
-//            head, whichever token it is.  e_t is taken into [-kScaleSpan, kScaleSpan], so that
-//            sums of p stay in fp32's range; where the tile's largest scale lies outside, w
-//            takes the rest of its exponent.
+//   softmax  per tile: with 2^e_t > sv_t and E the tile's largest e_t, the maximum Y of
+//            s_t + e_t - E over the 128 tokens (in powers of two; one redux per warp and head,
+//            one exchange through shared memory), p = 2^(s - Y), and w = p sv 2^(8 - E), whose
+//            largest then lies in [2^7, 2^8) for every head, whichever token it is.
 //   output   O^T[D x heads] = V-tile^T (A, read "transposed" as stored: D contiguous) . w.
 //            w is split into four E4M3 pieces w = c0 + c1/16 + c2/256 + c3/4096: off by at
 //            most 2^-17 relative, or 2^-29 of the head's largest w of the tile.  (With p taken
-//            from the largest score, and w from the tile's largest scale instead, a large scale
-//            with hardly any probability would cost the other tokens their bits.  The addition
-//            in front of the maximum costs 1.1 of 68.4 us with 16 heads a tile, nothing that
+//            from the largest score instead, w would be held to 2^-30 of the tile's largest sv:
+//            a large scale with hardly any probability would cost the other tokens their bits.
+//            The addition before the maximum costs 2.5 of 70 us with 16 heads a tile, nothing that
 //            shows with 4 or 8.)
 //            Each tile's product lands in fresh tensor-memory columns and is folded into fp32
 //            registers (one channel d per thread) with the running maximum's factors.
@@ -73,9 +71,13 @@ constexpr int kAttnTile = 128;
 // Tiles whose scales are held: a K-slot is filled for tile j only after the outputs of tile j - 4
 // (or a later one) have left a V-slot, whatever the ring's length.
 constexpr int kScaleRing = 4;
-// Binades of value scales to either side of 1 that the softmax's reference follows: sums of p
-// lie between 2^-kScaleSpan and 2^kScaleSpan times the number of tokens.
-constexpr int kScaleSpan = 80;
+// Binades by which value scales of a tile may differ before the smaller ones count as this far
+// from the largest.  Sums of p reach 2^kScaleSpread times the number of tokens (a token with
+// nearly all of the probability and the smallest scale), which fp32 has to hold: a tile whose
+// reference lies 2^126 below another's adds nothing, and it is at most 2^(kScaleSpread - 126) of
+// the sum.  (Scales that count with their own exponent, without the tile's largest, would move
+// the references of two tiles apart by twice the span and lose such a tile.)
+constexpr int kScaleSpread = 90;
 // Register split of the variant with 16 heads (the pool is kLaunchRegs a thread).
 constexpr uint32_t kAttnLoadRegs = 88, kAttnSoftmaxRegs = 208;
 static_assert(128 * kAttnLoadRegs + 256 * kAttnSoftmaxRegs <= 384 * kLaunchRegs, "register split exceeds pool");
@@ -133,7 +135,6 @@ struct AttnRange {
 template <int GT, int SLOTS>
 struct alignas(16) AttnState {            // arrays [2]: by warpgroup
   float red[2][2][4][GT];  // [parity of its tile]: per-warp maxima
-  float redsv[2][2][4];
   float lsum[2][4][GT];    // per-warp sums of p
   float cq[2][2][GT];      // per-head factor of the staged queries
   uint64_t full[2][SLOTS];
@@ -730,6 +731,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // ------------------------------------------------ softmax and accumulation
       const int quad = warp & 3;                   // tensor-memory lanes of this warp
       const int tok = quad * 32 + lane;            // token of the tile; channel of the output
+      const uint32_t all_boxes = (2u << (kAttnTile / a.BR - 1)) - 1u;
+      const int box4 = 4 * lane / a.BR;            // the box of tokens 4 lane .. 4 lane + 3
       const uint32_t tlane = uint32_t(quad * 32) << 16;
       const uint32_t tmem_s = tmem + tlane + 2 * wg * C::S_COLS;
       const uint32_t tmem_o = tmem + tlane + 4 * C::S_COLS + wg * (DCH * C::O_COLS);
@@ -793,7 +796,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t boxes = ps->boxes[wg][e];
           const bool live = t0 + tok >= w.s.st && t0 + tok < w.s.len && ((boxes >> (tok / a.BR)) & 1u);
           const float sk = live ? sc[tok] : 0.0f, sv = live ? sc[128 + tok] : 0.0f;
-          const float es = float(min(max(int(__float_as_uint(fabsf(sv)) >> 23) - 126, -kScaleSpan), kScaleSpan));
+          // the tile's largest sv, four tokens a lane (every warp for itself: no exchange), 2^E >= it
+          // (E >= -118, for which 2^(8 - E) is a number; a scale of 2^-126 is held to 2^-22), and
+          // this token's e_t - E
+          float top;
+          {
+            const float4 s4 = *reinterpret_cast<const float4*>(sc + 128 + 4 * lane);
+            // (64 x up to 8000 tokens, 2 heads of 64 a kv head: 69.3 us with the masks skipped in a tile
+            // that has none, 70.3 us without)
+            float v0 = fabsf(s4.x), v1 = fabsf(s4.y), v2 = fabsf(s4.z), v3 = fabsf(s4.w);
+            if (t0 < w.s.st || t0 + kAttnTile > w.s.len || boxes != all_boxes) {
+              const int t4 = t0 + 4 * lane, lo = w.s.st - t4;
+              const int hi = (boxes >> box4) & 1u ? w.s.len - t4 : 0;
+              v0 = lo <= 0 && hi > 0 ? v0 : 0.0f;
+              v1 = lo <= 1 && hi > 1 ? v1 : 0.0f;
+              v2 = lo <= 2 && hi > 2 ? v2 : 0.0f;
+              v3 = lo <= 3 && hi > 3 ? v3 : 0.0f;
+            }
+            top = warp_max(fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)));
+          }
+          const int etop = int(__float_as_uint(top) >> 23), E = max(etop - 126, -118);
+          const float apart =
+              float(min(max(int(__float_as_uint(fabsf(sv)) >> 23) - etop, -kScaleSpread), 0));
+          // (an infinite scale makes its token NaN: E4M3 would saturate without a trace)
+          const float rsv = fabsf(sv) == INFINITY ? NAN : sv * __uint_as_float(uint32_t(8 - E + 127) << 23);
+          const float down = __uint_as_float(uint32_t(E - 8 + 127) << 23);
           ok &= attn_wait(smem_u32(&ps->sfull[wg][par]), (j >> 1) & 1u, abort, limit);
           tc_fence_after();
           float x[GT];
@@ -808,29 +835,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const float2 v = unpack2(mul2(fma2(lo, pack2(0.0625f, 0.0625f), hi), mul2(cq[i], pack2(sk, sk))));
               x[2 * i] = live ? v.x : -INFINITY;
               x[2 * i + 1] = live ? v.y : -INFINITY;
-              const float2 y = unpack2(add2(pack2(x[2 * i], x[2 * i + 1]), pack2(es, es)));
+              const float2 y = unpack2(add2(pack2(x[2 * i], x[2 * i + 1]), pack2(apart, apart)));
               wm[2 * i] = warp_max(y.x);
               wm[2 * i + 1] = warp_max(y.y);
             }
-            const float wv = warp_max(fabsf(sv));
             if (lane == 0) {
 #pragma unroll
               for (int g = 0; g < GT; g += 4)
                 *reinterpret_cast<float4*>(&ps->red[wg][par][quad][g]) =
                     make_float4(wm[g], wm[g + 1], wm[g + 2], wm[g + 3]);
-              ps->redsv[wg][par][quad] = wv;
             }
           }
           if (t > t_first) accumulate(j - 1);
           ok = meet(ok);
           if (!ok) break;
-          // what the largest sv has beyond 2^kScaleSpan or less than 2^-kScaleSpan
-          const float4 vm = *reinterpret_cast<const float4*>(ps->redsv[wg][par]);
-          const int E = int(__float_as_uint(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))) >> 23) - 126;
-          const int rest = E - min(max(E, -kScaleSpan), kScaleSpan);
-          // (an infinite scale makes its token NaN: E4M3 would saturate without a trace)
-          const float rsv = fabsf(sv) == INFINITY ? NAN : sv * __uint_as_float(uint32_t(8 - rest + 127) << 23);
-          const float down = __uint_as_float(uint32_t(rest - 8 + 127) << 23);
           // lane i: the factors of head i % GT
           const int hg = lane & (GT - 1);
           const float tm = fmaxf(fmaxf(ps->red[wg][par][0][hg], ps->red[wg][par][1][hg]),

@@ -407,11 +407,11 @@ bool make_map_cache(CUtensorMap* m, const fp8_kv_cache* c, void* codes, uint32_t
 // Query heads of one kv head that a tile carries: the least of 4, 8 and 16 that holds them, or
 // several chunks of the largest (8 for heads of over 128 channels, whose tiles leave no shared
 // memory for more).  Up to one chunk the softmax's issue slots decide: 64 ragged sequences of up to
-// 8000 tokens with 2 heads of 64 channels a kv head take 68 us with tiles of 4 and 83 us with
+// 8000 tokens with 2 heads of 64 channels a kv head take 69 us with tiles of 4 and 83 us with
 // tiles of 8 (512 of up to 1000 tokens with 4 of 128: 127 and 138 us).  Every chunk is a row of
 // its own and loads its keys and values for itself, so the cache crosses the memory system once
-// per chunk: with 16 heads of 128 channels 121 us with tiles of 16 and 177 us with two of 8; 4 kv
-// heads of 128 with 32 heads each 124 us, with 16 each 68 us.
+// per chunk: with 16 heads of 128 channels 123 us with tiles of 16 and 177 us with two of 8; 4 kv
+// heads of 128 with 32 heads each 126 us, with 16 each 70 us.
 inline int attn_gt(int64_t G, int64_t D) { return G <= 4 ? 4 : G <= 8 || D > 128 ? 8 : 16; }
 inline int64_t attn_chunks(int64_t G, int64_t D) { return (G + attn_gt(G, D) - 1) / attn_gt(G, D); }
 

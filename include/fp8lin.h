@@ -435,10 +435,10 @@ int fp8_kv_read(const fp8_kv_cache* cache, const int32_t* table, int64_t table_s
  * Scores, softmax and sums are fp32.  q enters the first product exactly down to 2^-14 of its
  * head's largest element, and off by at most 2^-21 of that below.  Probability times v_scale
  * enters the second with 17 significant bits, or, where it is small against others, off by at
- * most 2^-29 of the head's largest among the tokens [128 i, 128 i + 128) it stands with.  (This
- * largest is of probability times v_scale taken into [2^-80, 2^80], times S over S taken into
- * the same, S the largest v_scale there.)  The result does not depend on timing.  A token that
- * counts and whose v_scale is infinite makes its row NaN.
+ * most 2^-29 of the head's largest among the tokens [128 i, 128 i + 128) it stands with (2^-21
+ * for v scales below 2^-118), provided that the v scales of a sequence and kv head are within
+ * 2^80 of one another.  The result does not depend on timing.  A token that counts and whose
+ * v_scale is infinite makes its row NaN.
  * fp8_paged_attention_ws_bytes returns 0 for a cache or counts that the call would refuse.
  */
 int64_t fp8_paged_attention_ws_bytes(int64_t B, int64_t Hq, const fp8_kv_cache* cache);
