@@ -105,3 +105,22 @@ def test_fused(cuda_device, T, Hq, H, D, r, interleaved, fmt, scale_fmt):
     assert torch.equal(qo, ref_q) and torch.equal(c.v, apart.v)
     assert torch.equal(c.v_scale.view(torch.int32), apart.v_scale.view(torch.int32))
     assert F.fp8_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 37, 2003])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_fused_with_q_in_place(cuda_device, T, interleaved):
+    """q rewritten inside the projection's output that k and v are views of: they stay."""
+    Hq, H, D, r, P = 7, 3, 96, 64, 16
+    qkv = rand((T, Hq + 2 * H, D), T + 9)
+    before = qkv.clone()
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:]
+    wq, wk = rand((1, D), 5)[0], rand((1, D), 6)[0]
+    pos, cs = tables(T, r, T)
+    slots = torch.arange(T, device="cuda")
+    c, d = (make_cache(-(-T // P), P, H, D) for _ in range(2))
+    ref = F.qk_norm_rope_kv_write(q, k, v, pos, cs, slots, c, wq, wk, EPS, interleaved)
+    F.fp8_qk_norm_rope_kv_write(q, k, v, pos, cs, slots, d, q, wq, wk, EPS, interleaved)
+    assert torch.equal(q, ref) and torch.equal(qkv[:, Hq:], before[:, Hq:])
+    assert torch.equal(c.k, d.k) and torch.equal(c.v, d.v)
+    assert F.fp8_device_error() == 0
